@@ -24,13 +24,18 @@ Functions mirror the C entry points:
 * :func:`int8_repack_qat`, :func:`int8_quant_act`, :func:`int8_rowwise_linear`
   (:func:`int8_rowwise_linear_ws` with a workspace),
   :func:`int8_linear` - the int8 W8A8 build.
+* :func:`rope` (tables: :func:`rope_frequencies`), :func:`kv_append`,
+  :func:`paged_attention` (:func:`paged_attention_workspace`) - the attention
+  block between the q/k/v linears and the o linear, on a paged bf16 cache.
 * :func:`device_status` - read and clear the device status word.
 """
 
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 
 import torch
 
@@ -82,6 +87,13 @@ _SIGS = {
     "int8_rowwise_linear": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _P], ctypes.c_int),
     "int8_rowwise_linear_ws": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "int8_linear_bf16": ([_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P], ctypes.c_int),
+    "bf16_rope": ([_P, _I64, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_int32, ctypes.c_float, _P, _I64, _P],
+                  ctypes.c_int),
+    "bf16_kv_append": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, ctypes.c_char_p, _P, _I64,
+                        ctypes.c_int32, ctypes.c_float, _P], ctypes.c_int),
+    "bf16_paged_attention_workspace_bytes": ([_I64], ctypes.c_size_t),
+    "bf16_paged_attention": ([_P, _I64, _I64, _I64, ctypes.c_char_p, _I64, ctypes.c_float, _I64, _P, _I64, _P, _P,
+                              ctypes.c_size_t, _P], ctypes.c_int),
 }
 for _name, (_args, _ret) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -526,6 +538,181 @@ def cast_e4m3(x: torch.Tensor, out: torch.Tensor | None = None):
     return out
 
 
+# ------------------------------------------------------------------ attention block
+_PAGED_KV = struct.Struct("@PP7qPqqPP")  # bf16_paged_kv
+
+
+def _on_current(t: torch.Tensor, dtype, name: str) -> torch.Tensor:
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def _heads(t: torch.Tensor, name: str, shape=None):
+    """Address and token pitch of a bf16 [T, heads, head_dim] tensor whose heads lie side by side."""
+    _on_current(t, torch.bfloat16, name)
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {'[T, heads, head_dim]' if shape is None else tuple(shape)}, "
+                         f"got {tuple(t.shape)}")
+    T, H, D = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * D
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError(f"{name}: the elements of a head and the heads of a token must lie side by side")
+    return t.data_ptr(), st[0] if T > 1 else H * D
+
+
+def _ints(t: torch.Tensor, name: str, n: int | None = None) -> int:
+    _on_current(t, torch.int32, name)
+    if not t.is_contiguous() or (n is not None and (t.dim() != 1 or t.shape[0] != n)):
+        raise ValueError(f"{name} must be contiguous" + ("" if n is None else f" with shape ({n},)"))
+    return t.data_ptr()
+
+
+def _frequencies(t: torch.Tensor, name: str) -> int:
+    _on_current(t, torch.float32, name)
+    if t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector")
+    return t.data_ptr()
+
+
+def _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, head_dim):
+    _on_current(k_cache, torch.bfloat16, "k_cache")
+    _on_current(v_cache, torch.bfloat16, "v_cache")
+    if k_cache.dim() != 4 or k_cache.shape[3] != head_dim:
+        raise ValueError(f"k_cache must be [pages, page_size, heads, {head_dim}], got {tuple(k_cache.shape)}")
+    pages, page_size, heads, _ = k_cache.shape
+    st = k_cache.stride()
+    if v_cache.shape != k_cache.shape or v_cache.stride() != st:
+        raise ValueError("v_cache must have the shape and strides of k_cache")
+    if st[3] != 1:
+        raise ValueError("k_cache: the elements of a head must lie side by side")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    batch, max_pages = page_table.shape
+    return _PAGED_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, heads, head_dim, st[0], st[1],
+                          st[2], _ints(page_table, "page_table"), batch, max_pages, _ints(cu_q, "cu_q", batch + 1),
+                          _ints(kv_lens, "kv_lens", batch))
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: int = 8192, low: float = 1.0, high: float = 4.0, device=None):
+    """The frequency table of :func:`rope` and :func:`kv_append` and the amplitude that belongs to it:
+    ``(inv_freq fp32 [rotary_dim / 2], amplitude)``, computed in fp64.
+
+    f_j = base^(-2j / rotary_dim), then for contexts ``factor`` times longer than ``original_length``:
+
+    * ``"none"``: as it is;
+    * ``"linear"``: f / factor (positions interpolated);
+    * ``"wavelength"``: by the turns n = original_length f / 2 pi that a pair makes over the original length: slowed
+      by the factor below ``low`` turns, unchanged above ``high``, in between (1 - r) f / factor + r f with
+      r = (n - low) / (high - low);
+    * ``"yarn"`` (Peng et al., YaRN): the ramp runs over the pair index instead, between the (fractional) indices of
+      ``high`` and ``low`` turns, rounded outwards, and amplitude = 0.1 ln(factor) + 1. Usual: low 1, high 32.
+    """
+    if rotary_dim < 2 or rotary_dim % 2 or base <= 1 or factor <= 0 or original_length <= 0 or not 0 < low < high:
+        raise ValueError("rotary_dim even, base > 1, factor > 0, original_length > 0 and 0 < low < high are needed")
+    j = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    f = base ** (-2.0 * j / rotary_dim)
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "wavelength":
+        r = ((original_length * f / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        f = (1 - r) * f / factor + r * f
+    elif scaling == "yarn":
+        index = [rotary_dim * math.log(original_length / (2 * math.pi * n)) / (2 * math.log(base)) for n in (high, low)]
+        lo, hi = max(math.floor(index[0]), 0), min(math.ceil(index[1]), rotary_dim - 1)
+        r = 1 - ((j - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        f = (1 - r) * f / factor + r * f
+        amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling != "none":
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(torch.float32).to(device or "cpu"), amplitude
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = False,
+         amplitude: float = 1.0, y: torch.Tensor | None = None):
+    """x bf16 [T, heads, head_dim] with the first 2 * len(inv_freq) elements of each head turned by positions int32 [T]
+    (y may be x)."""
+    xp, ldx = _heads(x, "x")
+    T, H, D = x.shape
+    y = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device) if y is None else y
+    yp, ldy = _heads(y, "y", x.shape)
+    _check(_lib.bf16_rope(xp, ldx, _ints(positions, "positions", T), _frequencies(inv_freq, "inv_freq"), T, H, D,
+                          2 * inv_freq.shape[0], interleaved, amplitude, yp, ldy, _stream()), "bf16_rope")
+    return y
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+              cu_q: torch.Tensor, kv_lens: torch.Tensor, inv_freq: torch.Tensor | None = None,
+              q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, interleaved: bool = False,
+              amplitude: float = 1.0):
+    """The new tokens' k and v bf16 [T, heads, head_dim] to their places in the paged cache ([pages, page_size, heads,
+    head_dim], any strides for the first three), the keys turned by their positions when inv_freq is given. With q
+    [T, q_heads, head_dim] the queries are turned too, into q_out (new when None; may be q), which is returned.
+    page_table int32 [batch, max_pages], cu_q int32 [batch + 1], kv_lens int32 [batch] (the new tokens counted)."""
+    kp, ldk = _heads(k, "k")
+    T, H, D = k.shape
+    vp, ldv = _heads(v, "v", k.shape)
+    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, D)
+    if k_cache.shape[2] != H:
+        raise ValueError(f"k has {H} heads, the cache {k_cache.shape[2]}")
+    qp = qop = None
+    ldq = ldqo = Hq = 0
+    if q is not None:
+        qp, ldq = _heads(q, "q")
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError(f"q must have shape ({T}, q_heads, {D}), got {tuple(q.shape)}")
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
+        qop, ldqo = _heads(q_out, "q_out", q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    R = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    _check(_lib.bf16_kv_append(kp, ldk, vp, ldv, qp, ldq, qop, ldqo, Hq, T, kv,
+                               None if inv_freq is None else _frequencies(inv_freq, "inv_freq"), R, interleaved,
+                               amplitude, _stream()), "bf16_kv_append")
+    return q_out
+
+
+def paged_attention_workspace(head_dim: int, device=None) -> torch.Tensor:
+    """A workspace for paged_attention on the current device, for any batch."""
+    n = int(_lib.bf16_paged_attention_workspace_bytes(head_dim))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                    cu_q: torch.Tensor, kv_lens: torch.Tensor, scale: float | None = None, window: int = 0,
+                    max_q: int | None = None, ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None):
+    """Attention of the new tokens' q bf16 [T, q_heads, head_dim] over the paged cache (see kv_append), causal, over the
+    last ``window`` keys when window > 0; scale defaults to head_dim^-0.5. max_q: no sequence has more new tokens
+    (None: T). lse fp32 [T, q_heads] receives ln sum exp of the scores when given. Returns out bf16 [T, q_heads,
+    head_dim]; rows behind cu_q[batch] stay as they are."""
+    qp, ldq = _heads(q, "q")
+    T, Hq, D = q.shape
+    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, D)
+    out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    op, ldo = _heads(out, "out", q.shape)
+    lp = None
+    if lse is not None:
+        _on_current(lse, torch.float32, "lse")
+        if lse.shape != (T, Hq) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous with shape ({T}, {Hq})")
+        lp = lse.data_ptr()
+    ws = paged_attention_workspace(D) if ws is None else _on_current(ws, torch.uint8, "ws")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    _check(_lib.bf16_paged_attention(qp, ldq, T, Hq, kv, 0 if max_q is None else max_q,
+                                     D ** -0.5 if scale is None else scale, window, op, ldo, lp, ws.data_ptr(),
+                                     ws.numel(), _stream()), "bf16_paged_attention")
+    return out
+
+
 __all__ = [
     "Fp8Error", "raw", "version", "device_supported", "device_status", "repack_qat",
     "convert_fnuz", "quant_act", "rowwise_linear", "rowwise_linear_ws", "linear_workspace", "linear",
@@ -534,6 +721,7 @@ __all__ = [
     "moe_route", "moe_gather", "grouped_linear", "moe_geglu_quant", "moe_combine",
     "moe_interleave_gate_up", "grouped_linear_geglu",
     "int8_repack_qat", "int8_quant_act", "int8_rowwise_linear", "int8_rowwise_linear_ws", "int8_linear",
+    "rope", "rope_frequencies", "kv_append", "paged_attention", "paged_attention_workspace",
     "bf16_linear", "moe_topk", "w4a16_dequant", "w4a16_workspace_bytes", "w4a16_linear",
     "DEV_NONFINITE", "DEV_NAN_CODE", "DEV_INEXACT", "DEV_TIMEOUT", "LIB_PATH",
 ]

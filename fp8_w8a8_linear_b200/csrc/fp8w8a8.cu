@@ -11,10 +11,12 @@
 #include <mutex>
 
 #include "../../include/fp8w8a8.h"
+#include "attn.cuh"
 #include "gemm.cuh"
 #include "moe.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
+#include "rope.cuh"
 #include "w4a16.cuh"
 
 namespace {
@@ -1395,4 +1397,156 @@ extern "C" fp8_status fp8_linear_bf16_noalloc(const uint16_t* x, const uint8_t* 
   if (fp8_status st = launch_quant_act(*dev, x, M, K, K, x8, s_tok, as_stream(stream))) return st;
   return launch_linear(*dev, x8, s_tok, w8, s_ch, static_cast<int>(M), static_cast<int>(N),
                        static_cast<int>(K), y, as_stream(stream), true);
+}
+
+// ============================================================ attention block
+namespace {
+
+// The cache and batch as the kernels see them, after the checks that the
+// append and the attention share.
+fp8_status paged_checked(const bf16_paged_kv* kv, int64_t T, PagedArgs* out) {
+  if (!kv) return FP8_ERR_INVALID_ARG;
+  if (!dims_ok(T, kMaxRows) || !dims_ok(kv->batch, kMaxRows) || !dims_ok(kv->max_pages, kMaxRows) ||
+      !dims_ok(kv->num_pages, kMaxRows) || kv->page_size < 1 || kv->page_size > (1 << 20) ||
+      kv->heads < 1 || kv->heads > 65536 || kv->head_dim < 1 || kv->page_stride < 0 ||
+      kv->token_stride < 0 || kv->head_stride < 0)
+    return FP8_ERR_INVALID_ARG;
+  if (kv->head_dim % 8 != 0 || kv->head_dim > 4096) return FP8_ERR_SHAPE;
+  // strides beyond 2^39 elements are beyond a tensor map (and any memory)
+  const int64_t lim = int64_t(1) << 38;
+  if (kv->page_stride > lim || kv->token_stride > lim || kv->head_stride > lim) return FP8_ERR_SHAPE;
+  if (kv->page_stride % 8 != 0 || kv->token_stride % 8 != 0 || kv->head_stride % 8 != 0)
+    return FP8_ERR_ALIGNMENT;
+  if (T > 0 && kv->batch > 0) {
+    if (!kv->cu_q || !kv->kv_lens) return FP8_ERR_INVALID_ARG;
+    if (kv->max_pages > 0 && !kv->page_table) return FP8_ERR_INVALID_ARG;
+    if (kv->num_pages > 0 && (!kv->k || !kv->v)) return FP8_ERR_INVALID_ARG;
+  }
+  if (!aligned16(kv->k) || !aligned16(kv->v) || !aligned4(kv->page_table) || !aligned4(kv->cu_q) ||
+      !aligned4(kv->kv_lens))
+    return FP8_ERR_ALIGNMENT;
+  out->k = kv->k;
+  out->v = kv->v;
+  out->num_pages = kv->num_pages;
+  out->page_stride = kv->page_stride;
+  out->token_stride = kv->token_stride;
+  out->head_stride = kv->head_stride;
+  out->page_size = static_cast<int>(kv->page_size);
+  out->heads = static_cast<int>(kv->heads);
+  out->D = static_cast<int>(kv->head_dim);
+  out->table = kv->page_table;
+  out->batch = static_cast<int>(kv->batch);
+  out->max_pages = static_cast<int>(kv->max_pages);
+  out->cu_q = kv->cu_q;
+  out->kv_lens = kv->kv_lens;
+  return FP8_OK;
+}
+
+fp8_status rope_checked(const float* inv_freq, int64_t head_dim, int64_t rotary_dim,
+                        int32_t interleaved, float amplitude, RopeArgs* out) {
+  if (rotary_dim < 0 || rotary_dim > head_dim) return FP8_ERR_INVALID_ARG;
+  if (rotary_dim % 16 != 0 || rotary_dim > kRopeMaxRotary) return FP8_ERR_SHAPE;
+  if (rotary_dim > 0 && !inv_freq) return FP8_ERR_INVALID_ARG;
+  if (!aligned4(inv_freq)) return FP8_ERR_ALIGNMENT;
+  out->inv_freq = inv_freq;
+  out->R = static_cast<int>(rotary_dim);
+  out->interleaved = interleaved != 0;
+  out->amplitude = amplitude;
+  return FP8_OK;
+}
+
+// A [T, heads, D] bf16 operand with token pitch ld.
+fp8_status rows_checked(const void* p, int64_t ld, int64_t heads, int64_t D) {
+  if (!p || ld < heads * D) return FP8_ERR_INVALID_ARG;
+  return aligned16(p) && ld % 8 == 0 ? FP8_OK : FP8_ERR_ALIGNMENT;
+}
+
+}  // namespace
+
+extern "C" fp8_status bf16_rope(const uint16_t* x, int64_t ldx, const int32_t* positions,
+                                const float* inv_freq, int64_t T, int64_t heads, int64_t head_dim,
+                                int64_t rotary_dim, int32_t interleaved, float amplitude,
+                                uint16_t* y, int64_t ldy, void* stream) {
+  if (!dims_ok(T, kMaxRows) || heads < 1 || heads > 65536 || head_dim < 1) return FP8_ERR_INVALID_ARG;
+  if (head_dim % 8 != 0 || head_dim > 4096) return FP8_ERR_SHAPE;
+  RopeArgs r;
+  if (fp8_status st = rope_checked(inv_freq, head_dim, rotary_dim, interleaved, amplitude, &r)) return st;
+  if (T == 0) return FP8_OK;
+  if (fp8_status st = rows_checked(x, ldx, heads, head_dim)) return st;
+  if (fp8_status st = rows_checked(y, ldy, heads, head_dim)) return st;
+  if (!positions) return FP8_ERR_INVALID_ARG;
+  if (!aligned4(positions)) return FP8_ERR_ALIGNMENT;
+  DeviceInfo* dev;
+  if (fp8_status st = device_info(&dev)) return st;
+  return launch_pdl(rope_kernel, dim3(static_cast<unsigned>(T)), dim3(kRopeThreads),
+                    as_stream(stream), x, ldx, positions, static_cast<int>(heads),
+                    static_cast<int>(head_dim), r, y, ldy);
+}
+
+extern "C" fp8_status bf16_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                                     const uint16_t* q, int64_t ldq, uint16_t* q_out,
+                                     int64_t ldq_out, int64_t q_heads, int64_t T,
+                                     const bf16_paged_kv* kv, const float* inv_freq,
+                                     int64_t rotary_dim, int32_t interleaved, float amplitude,
+                                     void* stream) {
+  PagedArgs c;
+  if (fp8_status st = paged_checked(kv, T, &c)) return st;
+  RopeArgs r;
+  if (fp8_status st = rope_checked(inv_freq, kv->head_dim, rotary_dim, interleaved, amplitude, &r))
+    return st;
+  if (q && (q_heads < 1 || q_heads > 65536)) return FP8_ERR_INVALID_ARG;
+  if (T == 0 || kv->batch == 0) return FP8_OK;
+  if (fp8_status st = rows_checked(k, ldk, kv->heads, kv->head_dim)) return st;
+  if (fp8_status st = rows_checked(v, ldv, kv->heads, kv->head_dim)) return st;
+  if (q) {
+    if (fp8_status st = rows_checked(q, ldq, q_heads, kv->head_dim)) return st;
+    if (fp8_status st = rows_checked(q_out, ldq_out, q_heads, kv->head_dim)) return st;
+  }
+  DeviceInfo* dev;
+  if (fp8_status st = device_info(&dev)) return st;
+  const AppendArgs a = {k, v, q, q_out, ldk, ldv, ldq, ldq_out, q ? static_cast<int>(q_heads) : 0,
+                        static_cast<int>(T)};
+  return launch_pdl(kv_append_kernel, dim3(static_cast<unsigned>(T)), dim3(kRopeThreads),
+                    as_stream(stream), a, c, r);
+}
+
+extern "C" size_t bf16_paged_attention_workspace_bytes(int64_t head_dim) {
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+  DeviceInfo* dev;
+  if (device_info(&dev) != FP8_OK) return 0;
+  return 16;
+}
+
+extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64_t T,
+                                           int64_t q_heads, const bf16_paged_kv* kv, int64_t max_q,
+                                           float scale, int64_t window, uint16_t* o, int64_t ldo,
+                                           float* lse, void* ws, size_t ws_bytes, void* stream) {
+  PagedArgs c;
+  if (fp8_status st = paged_checked(kv, T, &c)) return st;
+  if (q_heads < 1 || window < 0 || !(scale > 0.0f) || !(scale <= 3.4e38f)) return FP8_ERR_INVALID_ARG;
+  if ((c.D != 64 && c.D != 128 && c.D != 256) || c.page_size % 8 != 0 || q_heads % c.heads != 0 ||
+      q_heads / c.heads > 128)
+    return FP8_ERR_SHAPE;
+  if (T == 0 || kv->batch == 0) return FP8_OK;
+  if (fp8_status st = rows_checked(q, ldq, q_heads, c.D)) return st;
+  if (fp8_status st = rows_checked(o, ldo, q_heads, c.D)) return st;
+  if (!aligned4(lse) || !aligned16(ws)) return FP8_ERR_ALIGNMENT;
+  DeviceInfo* dev;
+  if (fp8_status st = device_info(&dev)) return st;
+  if (!ws || ws_bytes < bf16_paged_attention_workspace_bytes(c.D)) return FP8_ERR_INVALID_ARG;
+  AttnArgs a = {};
+  a.q = q;
+  a.ldq = ldq;
+  a.o = o;
+  a.ldo = ldo;
+  a.lse = lse;
+  a.T = static_cast<int>(T);
+  a.Hq = static_cast<int>(q_heads);
+  a.G = a.Hq / c.heads;
+  a.max_q = static_cast<int>(max_q <= 0 ? T : std::min(max_q, T));
+  a.window = window > 0 && window < kMaxRows ? static_cast<int>(window) : static_cast<int>(kMaxRows);
+  a.scale = scale;
+  const dim3 grid(static_cast<unsigned>((T * q_heads + 3) / 4));
+  const auto kernel = c.D == 64 ? attn_simple_kernel<64> : c.D == 128 ? attn_simple_kernel<128> : attn_simple_kernel<256>;
+  return launch_pdl(kernel, grid, dim3(128), as_stream(stream), a, c);
 }

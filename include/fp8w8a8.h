@@ -536,6 +536,123 @@ fp8_status int8_linear_bf16(const uint16_t* x, const int8_t* w8, const float* s_
 fp8_status fp8_linear_bf16_noalloc(const uint16_t* x, const uint8_t* w8, const float* s_ch,
                                    int64_t M, int64_t N, int64_t K, uint16_t* y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention block: what lies between the q/k/v linears and the o linear, on
+ * a paged cache. Source: model card header paragraph (tensors other than the
+ * Linear weights and their activations stay bf16): activations and cache are
+ * bf16. The pages describe no attention kernel; the formulas below are the
+ * reading used.
+ *
+ * Batch: sequence b owns the rows cu_q[b] .. cu_q[b+1]-1 of the new tokens
+ * (q_len = cu_q[b+1] - cu_q[b], 0 allowed) and holds kv_lens[b] keys, the new
+ * ones among them: new token i is at position kv_len - q_len + i. Rows at
+ * and past cu_q[batch] belong to no sequence and are left as they are. cu_q
+ * must not decrease, 0 <= cu_q <= T, and 0 <= kv_len <= max_pages *
+ * page_size: a sequence for which this does not hold is skipped (its rows
+ * are left as they are) and sets FP8_DEV_BAD_INDEX.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * bf16_paged_kv: a paged cache and the batch on it; a HOST struct that is
+ * read during the call, holding device pointers. Element (page, token, head,
+ * d) of k and of v is at page * page_stride + token * token_stride + head *
+ * head_stride + d, strides in elements: [pages, page_size, heads, head_dim],
+ * [pages, heads, page_size, head_dim] and slices of larger arrays are all
+ * expressed by them. Position j of sequence b is token j % page_size of page
+ * page_table[b * max_pages + j / page_size]. Table entries behind a
+ * sequence's last page are not read. The strides are multiples of 8 and the
+ * arrays 16-byte aligned.
+ */
+typedef struct bf16_paged_kv {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t num_pages, page_size, heads, head_dim;
+  int64_t page_stride, token_stride, head_stride;
+  const int32_t* page_table; /* [batch, max_pages] */
+  int64_t batch, max_pages;
+  const int32_t* cu_q;    /* [batch + 1] */
+  const int32_t* kv_lens; /* [batch] */
+} bf16_paged_kv;
+
+/*
+ * bf16_rope: rotary positions. For each token t and head h the first
+ * rotary_dim elements of x[t, h] turn pairwise by the angle p f_j, p =
+ * positions[t], f_j = inv_freq[j] (radians per position):
+ *   y1 = x1 c - x2 s, y2 = x2 c + x1 s, c = amplitude cos(p f_j), s =
+ *   amplitude sin(p f_j);
+ * pair j is elements (j, j + rotary_dim/2), or (2j, 2j+1) when interleaved;
+ * the elements from rotary_dim on are copied. The turn is formed in fp64, so
+ * far positions keep their accuracy; products and sums in fp32, one rounding
+ * to bf16. Scaling for long contexts is a matter of the table and the
+ * amplitude; a negative position turns back.
+ *   x [T, heads, head_dim] bf16, token pitch ldx elements; y likewise (ldy);
+ *   y may be x (in place, with the same pitch).
+ *   positions [T] int32; inv_freq [rotary_dim/2] fp32.
+ * Requires head_dim % 8 == 0, rotary_dim % 16 == 0 and <= 512, rotary_dim <=
+ * head_dim, pitches multiples of 8 and >= heads * head_dim, x and y 16-byte
+ * aligned.
+ */
+fp8_status bf16_rope(const uint16_t* x, int64_t ldx, const int32_t* positions,
+                     const float* inv_freq, int64_t T, int64_t heads, int64_t head_dim,
+                     int64_t rotary_dim, int32_t interleaved, float amplitude, uint16_t* y,
+                     int64_t ldy, void* stream);
+
+/*
+ * bf16_kv_append: the batch's new keys and values to their places in the
+ * cache, the keys turned by their positions as in bf16_rope (rotary_dim 0:
+ * not at all, inv_freq may be NULL). With q not NULL the queries are turned
+ * in the same launch: q_out = rope(q), as bf16_rope with the tokens'
+ * positions; q_out may be q. kv_lens counts the new tokens already.
+ *   k, v [T, heads, head_dim] bf16 (pitch ldk, ldv); q, q_out [T, q_heads,
+ *   head_dim] bf16 (pitch ldq, ldq_out).
+ * A new token whose position is negative (q_len > kv_len) or whose page is
+ * not in [0, num_pages) is not written (nor its query) and sets
+ * FP8_DEV_BAD_INDEX. Two places of the tables that are written by one call
+ * must not be the same. Requires head_dim and the pitches as in bf16_rope.
+ */
+fp8_status bf16_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                          const uint16_t* q, int64_t ldq, uint16_t* q_out, int64_t ldq_out,
+                          int64_t q_heads, int64_t T, const bf16_paged_kv* kv,
+                          const float* inv_freq, int64_t rotary_dim, int32_t interleaved,
+                          float amplitude, void* stream);
+
+/*
+ * bf16_paged_attention_workspace_bytes: size of the workspace of
+ * bf16_paged_attention on the current device for this head_dim, whatever the
+ * batch (0 where the call is refused). It needs no initial contents and
+ * holds nothing from one call to the next; calls that may run at the same
+ * time need workspaces of their own.
+ */
+size_t bf16_paged_attention_workspace_bytes(int64_t head_dim);
+
+/*
+ * bf16_paged_attention: attention of the new tokens over the cache. Query
+ * head h reads the keys and values of head h / (q_heads / heads). For the
+ * token at position p, over the keys j <= p of its sequence - with window >
+ * 0 only those with j > p - window:
+ *   s_j = scale * q . k_j,  o = sum_j softmax(s)_j v_j (bf16),
+ *   lse = ln sum_j exp(s_j) (fp32; not computed when NULL).
+ * A token that sees no key (q_len > kv_len) gets o = 0 and lse = -inf. The
+ * keys are walked once with a running maximum and sum; scores, statistics
+ * and o in fp32, the probabilities rounded to bf16 for their product with v.
+ * The sum order depends on the batch's lengths and the device alone, so
+ * results are bit-reproducible. Values behind kv_len, and keys and values
+ * that no new token of the sequence sees, have no influence whatever they
+ * hold; a non-finite key or value that one of the sequence's new tokens sees
+ * may reach the outputs of the others. A page entry outside [0, num_pages)
+ * sets FP8_DEV_BAD_INDEX and its sequence's outputs are unspecified.
+ *   q, o [T, q_heads, head_dim] bf16, token pitch ldq, ldo; lse [T, q_heads]
+ *   fp32. max_q: no sequence has more new tokens (<= 0: T is taken); one that
+ *   has is skipped as above. ws: see above, 16-byte aligned.
+ * Requires head_dim 64, 128 or 256; q_heads a multiple of heads, at most 128
+ * times; page_size % 8 == 0; scale > 0 and finite; q, o, k, v 16-byte
+ * aligned, ldq and ldo multiples of 8 and >= q_heads * head_dim.
+ */
+fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64_t T, int64_t q_heads,
+                                const bf16_paged_kv* kv, int64_t max_q, float scale,
+                                int64_t window, uint16_t* o, int64_t ldo, float* lse, void* ws,
+                                size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
