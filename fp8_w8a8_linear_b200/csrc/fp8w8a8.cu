@@ -32,6 +32,7 @@ struct DeviceInfo {
   int sm_count = 0;
   int smem_optin = 0;     // largest dynamic shared memory a block may opt into
   int pair_clusters = 0;  // co-resident 2-CTA clusters of the pair GEMM
+  int attn_rows_ctas[3] = {};  // co-resident CTAs of attn_rows_kernel, head_dim 64, 128, 256
   bool supported = false;
   bool attrs_set = false;
 };
@@ -214,6 +215,25 @@ fp8_status set_w4_attr(int smem_optin) {
              : FP8_ERR_CUDA;
 }
 
+// attn_rows_kernel's ring: about 96 KB and two CTAs per SM, or for wide heads
+// (whose o and q take the registers) 192 KB and one.
+constexpr int attn_rows_slots(int D) { return D == 64 ? 12 : 6; }
+
+template <int D>
+fp8_status set_attn_attr(int sm_count, int* ctas) {
+  constexpr int S = attn_rows_slots(D);
+  const int smem = static_cast<int>(RowsCfg<D, S>::kSmem);
+  int n = 0;
+  if (cudaFuncSetAttribute(attn_rows_kernel<D, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_rows_kernel<D, S>, kRowsThreads, smem) !=
+          cudaSuccess ||
+      n < 1)
+    return FP8_ERR_CUDA;
+  *ctas = n * sm_count;
+  return FP8_OK;
+}
+
 constexpr int kPairStages = 6;
 // Grouped pair launches: five stages, which leaves room for the epilogue's
 // second staging buffer per warp.
@@ -271,6 +291,9 @@ fp8_status device_info(DeviceInfo** out) {
     st = st != FP8_OK ? st : set_w4_attr<64, 4, 3>(so);
     st = st != FP8_OK ? st : set_w4_attr<64, 2, 2>(so);
     st = st != FP8_OK ? st : set_w4_attr<128, 4, 2>(so);
+    st = st != FP8_OK ? st : set_attn_attr<64>(d.sm_count, &d.attn_rows_ctas[0]);
+    st = st != FP8_OK ? st : set_attn_attr<128>(d.sm_count, &d.attn_rows_ctas[1]);
+    st = st != FP8_OK ? st : set_attn_attr<256>(d.sm_count, &d.attn_rows_ctas[2]);
     if (st == FP8_OK &&
         (cudaFuncSetAttribute(quant_act_staged_kernel<false>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1510,11 +1533,69 @@ extern "C" fp8_status bf16_kv_append(const uint16_t* k, int64_t ldk, const uint1
                     as_stream(stream), a, c, r);
 }
 
+namespace {
+
+int attn_width(int64_t D) { return D == 64 ? 0 : D == 128 ? 1 : D == 256 ? 2 : -1; }
+
+// Sections of the attention workspace: the parts' o, their (maximum, sum),
+// and one descriptor per CTA.
+struct AttnWs {
+  size_t o, ml, desc;
+  size_t total() const { return o + ml + desc; }
+};
+
+AttnWs attn_ws(const DeviceInfo& dev, int D) {
+  const size_t parts = 2 * static_cast<size_t>(dev.attn_rows_ctas[attn_width(D)]) * kRowsMax;
+  return {parts * D * 4, parts * 8, static_cast<size_t>(dev.attn_rows_ctas[attn_width(D)]) * sizeof(int4)};
+}
+
+// Map over one array of the paged cache for boxes of box_rows tokens of one
+// head of one page: [head_dim / 64][box_rows][64] bf16 with the 128-byte
+// swizzle (dimensions: 64 elements, token, group of 64, head, page). A size
+// of one makes its stride meaningless; no page at all gets a map that no
+// load uses.
+bool make_tmap_paged(CUtensorMap* m, const uint16_t* base, const PagedArgs& c, int box_rows,
+                     const void* stand_in) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const auto stride = [](int64_t n, int64_t st) { return static_cast<cuuint64_t>(n > 1 ? 2 * st : 128); };
+  const cuuint64_t pages = c.num_pages > 0 ? c.num_pages : 1;
+  cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.D / 64),
+                        static_cast<cuuint64_t>(c.heads), pages};
+  cuuint64_t strides[4] = {stride(c.page_size, c.token_stride), 128, stride(c.heads, c.head_stride),
+                           stride(c.num_pages, c.page_stride)};
+  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(c.D / 64), 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  std::memset(m, 0, sizeof(*m));
+  void* p = c.num_pages > 0 ? const_cast<uint16_t*>(base) : const_cast<void*>(stand_in);
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, p, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The items of at most 16 rows, then the join of what was cut.
+template <int D>
+fp8_status launch_attn_rows(const DeviceInfo& dev, AttnArgs a, const PagedArgs& c, cudaStream_t stream) {
+  constexpr int S = attn_rows_slots(D);
+  const int ctas = dev.attn_rows_ctas[attn_width(D)];
+  a.box_rows = std::min(kRowsBN, c.page_size & -c.page_size);
+  CUtensorMap tmK, tmV;
+  if (!make_tmap_paged(&tmK, c.k, c, a.box_rows, a.q) || !make_tmap_paged(&tmV, c.v, c, a.box_rows, a.q))
+    return FP8_ERR_CUDA;
+  if (fp8_status st = launch_pdl_smem(attn_rows_kernel<D, S>, dim3(ctas), dim3(kRowsThreads),
+                                      RowsCfg<D, S>::kSmem, stream, tmK, tmV, a, c))
+    return st;
+  const unsigned rows = static_cast<unsigned>(a.max_q * a.G);
+  return launch_pdl(attn_join_kernel<D, kRowsMax, 8>, dim3(ctas, rows), dim3(256), stream, a);
+}
+
+}  // namespace
+
 extern "C" size_t bf16_paged_attention_workspace_bytes(int64_t head_dim) {
-  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+  if (attn_width(head_dim) < 0) return 0;
   DeviceInfo* dev;
   if (device_info(&dev) != FP8_OK) return 0;
-  return 16;
+  return attn_ws(*dev, static_cast<int>(head_dim)).total();
 }
 
 extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64_t T,
@@ -1524,7 +1605,7 @@ extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64
   PagedArgs c;
   if (fp8_status st = paged_checked(kv, T, &c)) return st;
   if (q_heads < 1 || window < 0 || !(scale > 0.0f) || !(scale <= 3.4e38f)) return FP8_ERR_INVALID_ARG;
-  if ((c.D != 64 && c.D != 128 && c.D != 256) || c.page_size % 8 != 0 || q_heads % c.heads != 0 ||
+  if (attn_width(c.D) < 0 || c.page_size % 8 != 0 || q_heads % c.heads != 0 ||
       q_heads / c.heads > 128)
     return FP8_ERR_SHAPE;
   if (T == 0 || kv->batch == 0) return FP8_OK;
@@ -1533,7 +1614,8 @@ extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64
   if (!aligned4(lse) || !aligned16(ws)) return FP8_ERR_ALIGNMENT;
   DeviceInfo* dev;
   if (fp8_status st = device_info(&dev)) return st;
-  if (!ws || ws_bytes < bf16_paged_attention_workspace_bytes(c.D)) return FP8_ERR_INVALID_ARG;
+  const AttnWs need = attn_ws(*dev, c.D);
+  if (!ws || ws_bytes < need.total()) return FP8_ERR_INVALID_ARG;
   AttnArgs a = {};
   a.q = q;
   a.ldq = ldq;
@@ -1545,7 +1627,16 @@ extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64
   a.G = a.Hq / c.heads;
   a.max_q = static_cast<int>(max_q <= 0 ? T : std::min(max_q, T));
   a.window = window > 0 && window < kMaxRows ? static_cast<int>(window) : static_cast<int>(kMaxRows);
-  a.scale = scale;
+  a.scale_log2 = scale * 1.44269504088896341f;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.part_o = reinterpret_cast<float*>(w);
+  a.part_ml = reinterpret_cast<float2*>(w + need.o);
+  a.part_desc = reinterpret_cast<int4*>(w + need.o + need.ml);
+  if (static_cast<int64_t>(a.max_q) * a.G <= kRowsMax) {
+    if (c.D == 64) return launch_attn_rows<64>(*dev, a, c, as_stream(stream));
+    if (c.D == 128) return launch_attn_rows<128>(*dev, a, c, as_stream(stream));
+    return launch_attn_rows<256>(*dev, a, c, as_stream(stream));
+  }
   const dim3 grid(static_cast<unsigned>((T * q_heads + 3) / 4));
   const auto kernel = c.D == 64 ? attn_simple_kernel<64> : c.D == 128 ? attn_simple_kernel<128> : attn_simple_kernel<256>;
   return launch_pdl(kernel, grid, dim3(128), as_stream(stream), a, c);
