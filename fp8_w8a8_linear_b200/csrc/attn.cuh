@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a) {
 #pragma unroll 4
     for (int i = first; i < n; i += WPR) {
       const float f = __shfl_sync(0xFFFFFFFFu, f_l, i);
+      if (f == 0.0f) continue;  // a part in which the row saw no key may have no o
       const float* p = a.part_o + (static_cast<int64_t>(slot(i0 + i)) * ROWS + r) * D + lane * (E < 4 ? E : 4);
       if constexpr (E == 2) {
         const float2 v = *reinterpret_cast<const float2*>(p);
@@ -616,50 +617,661 @@ __global__ void __launch_bounds__(kRowsThreads)
   if (!desc_written && threadIdx.x == 0) a.part_desc[cta] = make_int4(0, 0, 0, 0);
 }
 
-// One warp per (row, head); lane l holds elements l D/32 .. of q and o.
+// ------------------------------------------------------------------ many rows
+// attn_chunk_kernel: items of up to NT x 128 rows on the tensor cores. Per
+// tile of 128 rows (128 / G tokens times the G heads of a group) and 128 keys:
+//   S = Q K^T        tcgen05, both operands in shared memory, S in TMEM;
+//   softmax          one thread per row: 128 scores from TMEM to registers,
+//                    P (bf16) back to TMEM over S;
+//   O += P V         tcgen05, P from TMEM, V (keys x D) as a transposed
+//                    operand, O in TMEM.
+// Warps: four per row tile for the softmax, one that issues the MMAs, one that
+// loads. head_dim <= 128: two row tiles, so that one's softmax runs under the
+// other's MMAs. head_dim 256: o takes half of TMEM, so one row tile with two
+// buffers for S - the scores of the next keys are formed while the softmax
+// works on these. O is rescaled only when a row's maximum has grown by more
+// than 2^8 since the last time (the factor cancels in the end, and 2^8 times
+// a probability is as exact in bf16 and far from overflow in the sums): after
+// the first tiles hardly ever, so the softmax threads do it themselves.
+constexpr int kChunkBN = 128;
+
 template <int D>
-__global__ void __launch_bounds__(128) attn_simple_kernel(AttnArgs a, PagedArgs c) {
-  constexpr int E = D / 32;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (w >= static_cast<int64_t>(a.T) * a.Hq) return;
-  const int t = static_cast<int>(w / a.Hq), h = static_cast<int>(w % a.Hq);
-  int b = 0;
-  for (int i0 = 0; i0 < c.batch; i0 += 32)
-    b += __popc(__ballot_sync(0xFFFFFFFFu, i0 + lane < c.batch && c.cu_q[min(i0 + lane, c.batch - 1) + 1] <= t));
-  if (b >= c.batch) return;
-  const int q0 = c.cu_q[b], q1 = c.cu_q[b + 1], len = c.kv_lens[b];
-  if (!seq_ok(c, q0, q1, len, a.T) || q0 > t || t >= q1 || q1 - q0 > a.max_q) {
-    if (lane == 0) report(FP8_DEV_BAD_INDEX);
-    return;
+struct ChunkCfg {
+  static constexpr int kNT = D == 256 ? 1 : 2;    // row tiles of an item
+  static constexpr int kParts = D == 256 ? 2 : 1;  // slots per key tile and per value tile
+  static constexpr int kSlots = D == 64 ? 10 : 5;
+  static constexpr int kSlotBytes = 128 * (D < 128 ? D : 128) * 2;
+  static constexpr int kKCols = D < 128 ? D : 128;   // head elements of a key slot
+  static constexpr int kVKeys = kChunkBN / kParts;   // keys of a value slot
+  static constexpr int kQBytes = kNT * 128 * D * 2;
+  static constexpr int kThreads = kNT * 128 + 64;
+  static constexpr int kRows = kNT * 128;            // rows of a part in the workspace
+  static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kSlots) * kSlotBytes +
+                                  8 * (2 * kSlots + 10) + 32 + sizeof(PlanSmem<kThreads>);
+};
+
+// sum_{i < n} floor((a i + b) / m), a, b >= 0 (the Euclid-like recursion on
+// lattice points under a line).
+__device__ __forceinline__ long long floor_sum(long long n, uint32_t m, uint32_t a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const uint32_t t = m;
+    m = a;
+    a = t;
   }
-  const int p = len - q1 + t;
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
-  for (int e = 0; e < E; ++e) {
-    q[e] = __uint_as_float(static_cast<uint32_t>(a.q[t * a.ldq + h * D + lane * E + e]) << 16) * a.scale_log2;
-    o[e] = 0.0f;
+  return s;
+}
+
+// Key tiles of a sequence's first j blocks of tt new tokens (nb blocks in
+// all; first = the first new token's position). Block i sees the keys from
+// max(0, first + i tt - window + 1) to its last token, in tiles of 128, and
+// takes one tile where it sees none.
+__device__ __forceinline__ long long chunk_prefix(int first, int len, int window, int tt, int nb, int j) {
+  if (len == 0 || j == 0) return j;
+  const long long f = first;
+  const int je = f < 0 ? static_cast<int>(min(static_cast<long long>(j), -f / tt)) : 0;
+  const bool last = j == nb;  // the last block ends at len
+  long long s = je + floor_sum(j - (last ? 1 : 0) - je, kChunkBN, tt, f + (je + 1ll) * tt + kChunkBN - 1);
+  if (last) s += (len + static_cast<long long>(kChunkBN) - 1) / kChunkBN;
+  const long long x = window - 1 - f;
+  const long long jw = max(static_cast<long long>(je), x < 0 ? 0ll : x / tt + 1);
+  if (j > jw) s -= floor_sum(j - jw, kChunkBN, tt, f + jw * tt - window + 1);
+  return s;
+}
+
+// A run's segments: tiles t .. of item (sequence b, head h, block j).
+struct ChunkWalk {
+  int b, h, j, t, left;
+  int q0, ql, len, first, nb;  // the sequence
+  int lo_seq;                  // keys below it no new token sees
+  int tt;
+  int tok0, ntok, tile0, n;    // the item: tokens tok0 .. of the sequence, key tiles tile0 .. + n
+
+  __device__ __forceinline__ bool seq(const AttnArgs& a, const PagedArgs& c) {
+    const SeqSpan s = seq_span(a, c, b, kChunkBN);
+    q0 = s.q0, ql = s.ql, len = s.len;
+    first = len - ql;
+    lo_seq = s.lo;
+    nb = (ql + tt - 1) / tt;
+    return ql > 0;
   }
-  for (int j = max(0, p - a.window + 1); j <= p; ++j) {
-    const int32_t page = c.table[static_cast<int64_t>(b) * c.max_pages + j / c.page_size];
-    if (page < 0 || page >= c.num_pages) {
-      if (lane == 0) report(FP8_DEV_BAD_INDEX);
-      continue;
+  __device__ __forceinline__ void item(const AttnArgs& a) {
+    tok0 = j * tt;
+    ntok = min(ql - tok0, tt);
+    const long long p0 = static_cast<long long>(first) + tok0;
+    const int lo = static_cast<int>(max(0ll, p0 - a.window + 1));
+    const int hi = max(0, first + tok0 + ntok);
+    tile0 = lo / kChunkBN;
+    n = max(1, (hi + kChunkBN - 1) / kChunkBN - tile0);
+  }
+  // Whole warps call it (the search for the block uses the lanes).
+  __device__ __forceinline__ ChunkWalk(const AttnArgs& a, const PagedArgs& c, const AttnRun& r, int tt_) {
+    tt = tt_;
+    b = r.seq, left = r.units, h = 0, j = 0, t = 0;
+    if (left <= 0) return;
+    seq(a, c);
+    const long long per_head = chunk_prefix(first, len, a.window, tt, nb, nb);
+    h = static_cast<int>(r.sub_off / per_head);
+    const long long off = r.sub_off % per_head;
+    // the last block whose tiles start at or before off: 32 probes a round
+    int lo = 0, hi = nb;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int probe = lo + step * static_cast<int>(lane_id());
+      const bool le = probe < hi && chunk_prefix(first, len, a.window, tt, nb, probe) <= off;
+      const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, le));  // lane 0's probe is lo: always at or below
+      lo += step * k;
+      hi = min(hi, lo + step);
     }
-    const int64_t at = page * c.page_stride + (j % c.page_size) * c.token_stride + h / a.G * c.head_stride + lane * E;
-    float s = 0.0f;
-    for (int e = 0; e < E; ++e) s += q[e] * __uint_as_float(static_cast<uint32_t>(c.k[at + e]) << 16);
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    const float mn = fmaxf(m, s);
-    const float f = exp2f(m - mn), pr = exp2f(s - mn);
-    l = l * f + pr;
-    m = mn;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + pr * __uint_as_float(static_cast<uint32_t>(c.v[at + e]) << 16);
+    j = lo;
+    t = static_cast<int>(off - chunk_prefix(first, len, a.window, tt, nb, j));
+    item(a);
   }
-  for (int e = 0; e < E; ++e)
-    a.o[t * a.ldo + h * D + lane * E + e] = f32_to_bf16_rn(l > 0.0f ? o[e] / l : 0.0f);
-  if (a.lse && lane == 0) a.lse[static_cast<int64_t>(t) * a.Hq + h] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  __device__ __forceinline__ int seg() const { return min(left, n - t); }
+  __device__ __forceinline__ void next(const AttnArgs& a, const PagedArgs& c, int m) {
+    left -= m;
+    t = 0;
+    if (left <= 0) return;
+    if (++j == nb) {
+      j = 0;
+      if (++h == c.heads) {
+        h = 0;
+        do {
+          if (++b >= c.batch) {
+            left = 0;
+            return;
+          }
+        } while (!seq(a, c));
+      }
+    }
+    item(a);
+  }
+  // Row tile i (tt1 tokens each): its tokens, and the iterations [from, to)
+  // of the segment's m tiles in which it sees keys.
+  __device__ __forceinline__ int tile_tokens(int i, int tt1) const { return max(0, min(tt1, ntok - i * tt1)); }
+  __device__ __forceinline__ void tile_range(const AttnArgs& a, int i, int tt1, int m, int& from, int& to) const {
+    const int nt = tile_tokens(i, tt1);
+    from = to = 0;
+    if (nt == 0) return;
+    const int p0 = first + tok0 + i * tt1;
+    const int lo = static_cast<int>(max(0ll, static_cast<long long>(p0) - a.window + 1)) / kChunkBN;
+    const int hi = max(lo + 1, (max(0, p0 + nt) + kChunkBN - 1) / kChunkBN);
+    from = max(0, lo - tile0 - t);
+    to = min(m, hi - tile0 - t);
+    if (to < from) to = from;
+  }
+};
+
+// ---- tcgen05 with A in TMEM, TMEM stores, transposed-B descriptor
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Descriptor of an operand tile whose contiguous dimension is M/N (not K),
+// written by TMA with the 128-byte swizzle: 64 elements of M/N by eight of K
+// make a 1024-byte atom; lead_bytes from one group of 64 to the next, 1024
+// from eight of K to the next eight.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t lead_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lead_bytes >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+constexpr uint32_t kIdescBMnMajor = 1u << 16;  // operand B's contiguous dimension is N
+
+// 5-D tiled load, coordinates (0, token, group of 64, head, page).
+__device__ __forceinline__ void tma_load_page_cols(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                   int32_t token, int32_t group, int32_t head,
+                                                   int32_t page) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(token), "r"(group), "r"(head),
+      "r"(page)
+      : "memory");
+}
+// 4-D tiled load of queries, coordinates (0, head, token, group of 64).
+__device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                           int32_t head, int32_t token, int32_t group) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(head), "r"(token), "r"(group)
+      : "memory");
+}
+
+// Two products plus a shared pair: d = a * b + c per lane.
+__device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\t"
+      "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %4};\n\tmov.b64 pc, {%5, %5};\n\t"
+      "fma.rn.f32x2 pd, pa, pb, pc;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+// The softmax of one row tile's rows, one thread per row.
+template <int D>
+__device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs& c, ChunkWalk& w, int tile,
+                                              int tt1, uint32_t tmem, uint32_t s_full, uint32_t p_full,
+                                              uint32_t o_done, uint32_t abort_w, int per) {
+  using C = ChunkCfg<D>;
+  const int lane = lane_id(), quad = warp_id() & 3;
+  const int rr = 32 * quad + lane;  // row of the tile
+  const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+  const uint32_t o_addr = tmem + lanes + 256 + tile * D;
+  const int cta = blockIdx.x;
+  uint32_t count[2] = {0, 0};  // uses of the S buffers
+  uint32_t done = 0;           // products with V so far
+  bool ok = true;
+  int4 desc = make_int4(0, 0, 0, 0);
+  for (bool first_seg = true; w.left > 0 && ok; first_seg = false) {
+    const int m = w.seg();
+    int from, to;
+    w.tile_range(a, tile, tt1, m, from, to);
+    const int ntok = w.tile_tokens(tile, tt1);
+    const int p0 = w.first + w.tok0 + tile * tt1;  // positions p0 .. p0 + ntok - 1
+    const int pos = p0 + rr / a.G;
+    float mu = -INFINITY, l = 0.0f;
+    for (int i = from; i < to; ++i) {
+      const int buf = C::kNT == 2 ? tile : i & 1;
+      const uint32_t s_addr = tmem + lanes + 128 * buf;
+      const int key0 = (w.tile0 + w.t + i) * kChunkBN;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(s_full + 8 * buf, count[buf] & 1, abort_w));
+      if (!ok) break;
+      ++count[buf];
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s[q]);
+      tmem_ld_wait();
+      if (key0 + kChunkBN - 1 > p0 || p0 + ntok - 1 - key0 >= a.window) {  // some row's edge
+        const int rel = pos - key0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (static_cast<uint32_t>(rel - (32 * q + e)) >= static_cast<uint32_t>(a.window))
+              s[q][e] = 0xFF800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+        for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][e]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      const bool grow = top > mu + 8.0f;
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float nm = grow ? top : mu;
+        const float f = grow ? ex2(mu - nm) : 1.0f;  // mu = -inf: 0 (l and o are 0)
+        l *= f;
+        mu = nm;
+        if (i > from) {  // o holds the earlier keys: wait for their product
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(o_done, (done - 1) & 1, abort_w));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int cb = 0; cb < D; cb += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_addr + cb, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(o_addr + cb, o);
+          }
+        }
+      }
+      const float shift = mu == -INFINITY ? 0.0f : -mu;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]), a.scale_log2, shift);
+          x0 = ex2(x0);
+          x1 = ex2(x1);
+          sum[q] += x0 + x1;
+          pk[e / 2] = pack_bf16x2(x0, x1);
+        }
+        tmem_st16(s_addr + 16 * q, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + 8 * buf);
+      ++done;
+    }
+    if (!ok) break;
+    // ---- the segment's o
+    const bool whole = w.t == 0 && m == w.n;
+    const int part = 2 * cta + (first_seg ? 0 : 1);
+    const bool live = rr < ntok * a.G;  // ntok <= tt1
+    const int row = tile * tt1 * a.G + rr;
+    const int64_t tok = w.q0 + w.tok0 + tile * tt1 + rr / a.G;
+    const int head = w.h * a.G + rr % a.G;
+    if (to > from) {
+      // The last product, by way of the one before it: with two buffers for S
+      // neither need be done yet, and a parity tells only adjacent phases apart.
+      if (C::kNT == 1 && to - from > 1) ok = mbar_wait_ab(o_done, done & 1, abort_w);
+      ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_ab(o_done, (done - 1) & 1, abort_w));
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll 1
+      for (int cb = 0; cb < D; cb += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_addr + cb, o);
+        tmem_ld_wait();
+        if (live && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.o + tok * a.ldo + static_cast<int64_t>(head) * D + cb);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * q + e]) * inv;
+            dst[q] = f32_to_bf16x8(v);
+          }
+        } else if (live) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(part) * C::kRows + row) * D + cb);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                 __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+        }
+      }
+      tc_fence_before();
+    }
+    if (live) {
+      if (!whole)
+        a.part_ml[static_cast<int64_t>(part) * C::kRows + row] = make_float2(mu, l);
+      else if (a.lse)
+        a.lse[tok * a.Hq + head] = l > 0.0f ? (mu + log2f(l)) * kLn2 : -INFINITY;
+    }
+    if (w.t == 0 && !whole)
+      desc = join_desc((w.n - m + per - 1) / per, part, w.q0 + w.tok0, w.h * a.G, w.ntok * a.G);
+    w.next(a, c, m);
+  }
+  if (tile == 0 && rr == 0) a.part_desc[cta] = ok ? desc : make_int4(0, 0, 0, 0);
+}
+
+template <int D>
+__global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
+    attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const AttnArgs a, const PagedArgs c) {
+  using C = ChunkCfg<D>;
+  constexpr int NT = C::kNT, NS = C::kSlots, PARTS = C::kParts;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* slots = smem + C::kQBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(slots + NS * C::kSlotBytes);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * NS;
+  const uint32_t q_full = empty0 + 8 * NS, q_empty = q_full + 8;
+  const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_done = p_full + 16, drained = o_done + 16;
+  uint32_t* words = reinterpret_cast<uint32_t*>(bars + 2 * NS + 10);
+  const uint32_t abort_w = smem_u32(words);
+  uint32_t* tmem_holder = words + 1;
+  auto* plan = reinterpret_cast<PlanSmem<C::kThreads>*>(words + 8);
+  const uint32_t q_smem = smem_u32(smem), slot0 = smem_u32(slots);
+  const int warp = warp_id(), lane = lane_id();
+  constexpr int kMmaWarp = NT * 4, kLoadWarp = NT * 4 + 1;
+
+  if (threadIdx.x == 0) {
+    st_shared_volatile_u32(abort_w, 0u);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(drained, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(o_done + 8 * i, 1);
+    }
+    fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_launch_dependents();  // this CTA holds its TMEM
+  pdl_wait();
+  const int tt1 = 128 / a.G, tt = NT * tt1;
+  const AttnRun run = find_run<C::kThreads>(*plan, c.batch, blockIdx.x, gridDim.x, [&](int b) -> long long {
+    const SeqSpan s = seq_span(a, c, b, kChunkBN);
+    if (!s.ok && blockIdx.x == 0) report(FP8_DEV_BAD_INDEX);
+    if (s.ql == 0) return 0;
+    const int nb = (s.ql + tt - 1) / tt;
+    return chunk_prefix(s.len - s.ql, s.len, a.window, tt, nb, nb) * c.heads;
+  });
+  ChunkWalk w(a, c, run, tt);
+
+  if (warp < kMmaWarp) {
+    const int tile = warp >> 2;
+    chunk_softmax<D>(a, c, w, tile, tt1, tmem, s_full, p_full, o_done + 8 * tile, abort_w, run.per);
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------- MMA issue
+    constexpr uint32_t kIdescS = idesc_kind<kKindBF16>(128, kChunkBN);
+    constexpr uint32_t kIdescO = idesc_kind<kKindBF16>(128, D) | kIdescBMnMajor;
+    int slot = 0;            // next slot in load order
+    uint32_t phase = 0;
+    uint32_t q_count = 0, p_count[2] = {0, 0};
+    bool ok = true, issued = false;
+    const auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(bar, parity, abort_w));
+      return ok;
+    };
+    // Waits for the next PARTS slots and returns the first; they are used in
+    // load order.
+    const auto take = [&](int (&at)[PARTS]) {
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        at[p] = slot;
+        wait(full0 + 8 * slot, phase);
+        if (++slot == NS) slot = 0, phase ^= 1;
+      }
+    };
+    const auto release = [&](const int (&at)[PARTS]) {
+      if (ok && lane == 0)
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) umma_commit(empty0 + 8 * at[p]);
+    };
+    const auto release_q = [&] {  // after the segment's last scores
+      if (ok && lane == 0) umma_commit(q_empty);
+    };
+    const auto scores = [&](int tile, int buf, const int (&at)[PARTS]) {
+      if (ok && lane == 0) {
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t qa = q_smem + tile * (128 * D * 2) + (k >> 2) * 16384 + (k & 3) * 32;
+          const int p = k * 16 / C::kKCols, kk = k - p * (C::kKCols / 16);
+          const uint32_t kb = slot0 + at[p] * C::kSlotBytes + (kk >> 2) * 16384 + (kk & 3) * 32;
+          umma_kind<kKindBF16>(tmem + 128 * buf, sw128_kmajor_desc(qa), sw128_kmajor_desc(kb), kIdescS, k > 0);
+        }
+        umma_commit(s_full + 8 * buf);
+      }
+      issued = true;
+    };
+    const auto product = [&](int tile, int buf, const int (&at)[PARTS], bool add) {
+      if (ok && lane == 0) {
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kChunkBN / 16; ++k) {
+          const int p = k * 16 / C::kVKeys, kk = k - p * (C::kVKeys / 16);
+          umma_bf16_ts(tmem + 256 + tile * D, tmem + 128 * buf + 8 * k,
+                       sw128_mnmajor_desc(slot0 + at[p] * C::kSlotBytes + kk * 2048, C::kVKeys * 128), kIdescO,
+                       add || k > 0);
+        }
+        umma_commit(o_done + 8 * tile);
+      }
+    };
+    // Value rows that are not keys of the sequence's new tokens hold anything
+    // (or were not loaded): zeros, which the zero probabilities leave alone.
+    const auto clear = [&](const int (&at)[PARTS], int key0) {
+      const int lo = w.lo_seq - key0, hi = w.len - key0;  // rows [lo, hi) count
+      if (lo <= 0 && hi >= kChunkBN) return;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+        for (int r = 0; r < C::kVKeys; ++r) {
+          const int key = p * C::kVKeys + r;
+          if (key >= lo && key < hi) continue;
+          if (lane < D / 8)
+            *reinterpret_cast<uint4*>(slots + at[p] * C::kSlotBytes + (lane >> 3) * (C::kVKeys * 128) + r * 128 +
+                                      (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+      fence_proxy_async_shared();
+      __syncwarp();
+    };
+    while (w.left > 0 && ok) {
+      const int m = w.seg();
+      int from[NT], to[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) w.tile_range(a, i, tt1, m, from[i], to[i]);
+      const int tile_first = w.tile0 + w.t;
+      wait(q_full, q_count & 1);
+      ++q_count;
+      int kat[PARTS], vat[PARTS];
+      take(kat);
+      if constexpr (NT == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (from[i] == 0 && to[i] > 0) scores(i, i, kat);
+        release(kat);
+        if (m == 1) release_q();
+        for (int n = 0; n < m && ok; ++n) {
+          take(vat);
+          clear(vat, (tile_first + n) * kChunkBN);
+          bool next = n + 1 < m;
+          if (next) take(kat);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (n >= from[i] && n < to[i]) {
+              wait(p_full + 8 * i, p_count[i] & 1);
+              ++p_count[i];
+              product(i, i, vat, n > from[i]);
+            }
+            if (next && n + 1 >= from[i] && n + 1 < to[i]) scores(i, i, kat);
+          }
+          if (next) release(kat);
+          if (n + 2 == m) release_q();
+          release(vat);
+        }
+      } else {
+        scores(0, 0, kat);
+        release(kat);
+        if (m == 1) release_q();
+        for (int n = 0; n < m && ok; ++n) {
+          if (n + 1 < m) {
+            take(kat);
+            scores(0, (n + 1) & 1, kat);
+            release(kat);
+            if (n + 2 == m) release_q();
+          }
+          take(vat);
+          clear(vat, (tile_first + n) * kChunkBN);
+          wait(p_full + 8 * (n & 1), p_count[n & 1] & 1);
+          ++p_count[n & 1];
+          product(0, n & 1, vat, n > 0);
+          release(vat);
+        }
+      }
+      w.next(a, c, m);
+    }
+    if (!ok && issued && lane == 0) {
+      // everything issued is done before TMEM is given back (bounded)
+      umma_commit(drained);
+      mbar_wait(drained, 0);
+    }
+  } else if (warp == kLoadWarp) {
+    // ------------------------------------------------------------- loads
+    const int rows = a.box_rows;
+    constexpr int kColGroups = C::kKCols / 64, kAllGroups = D / 64;
+    const uint32_t box_bytes = static_cast<uint32_t>(rows) * 128;
+    int slot = 0, filled = 0;
+    uint32_t phase = 0, q_count = 0;
+    bool ok = true;
+    const auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(bar, parity, abort_w));
+      return ok;
+    };
+    // lane l: the page of piece l (rows tokens) of a tile; negative: not loaded
+    const auto pages_of = [&](int tile) {
+      const uint32_t tok = static_cast<uint32_t>(tile) * kChunkBN + lane * rows;
+      int page = -2;
+      if (lane * rows < kChunkBN && tok < static_cast<uint32_t>(w.len) &&
+          tok + rows > static_cast<uint32_t>(w.lo_seq)) {
+        page = c.table[static_cast<int64_t>(w.b) * c.max_pages + tok / c.page_size];
+        if (page < 0 || page >= c.num_pages) {
+          report(FP8_DEV_BAD_INDEX);
+          page = -1;
+        }
+      }
+      return page;
+    };
+    // One slot: `groups` column groups from group g0 of the pieces from piece p0 on.
+    const auto load = [&](const CUtensorMap* map, int tile, int pages, int p0, int pieces, int g0, int groups) {
+      const int piece = p0 + lane / groups, grp = lane % groups;
+      const int page = __shfl_sync(0xFFFFFFFFu, pages, piece & 31);
+      const bool mine = lane < pieces * groups && page >= 0;
+      const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes;
+      if (filled >= NS && !wait(empty0 + 8 * slot, phase ^ 1)) return;
+      if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot, bytes);
+      __syncwarp();
+      if (mine) {
+        const int in_page = static_cast<int>((static_cast<uint32_t>(tile) * kChunkBN + piece * rows) % c.page_size);
+        tma_load_page_cols(slot0 + slot * C::kSlotBytes + grp * (pieces * box_bytes) + (piece - p0) * box_bytes, map,
+                           full0 + 8 * slot, in_page, g0 + grp, w.h, page);
+      }
+      ++filled;
+      if (++slot == NS) slot = 0, phase ^= 1;
+    };
+    const auto load_k = [&](int tile, int pages) {
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+        if (ok) load(&tmK, tile, pages, 0, kChunkBN / rows, p * kColGroups, kColGroups);
+    };
+    const auto load_v = [&](int tile, int pages) {
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+        if (ok) load(&tmV, tile, pages, p * (C::kVKeys / rows), C::kVKeys / rows, 0, kAllGroups);
+    };
+    while (w.left > 0 && ok) {
+      const int m = w.seg();
+      const int tile = w.tile0 + w.t;
+      int pg = pages_of(tile);
+      load_k(tile, pg);
+      if (q_count > 0) wait(q_empty, (q_count - 1) & 1);
+      if (ok) ++q_count;
+      if (ok) {
+        const int nq = w.tile_tokens(1, tt1) > 0 && NT == 2 ? 2 : 1;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nq) * kAllGroups * tt1 * a.G * 128);
+        __syncwarp();
+        if (lane < nq * kAllGroups) {
+          const int i = lane / kAllGroups, grp = lane % kAllGroups;
+          tma_load_q(q_smem + i * (128 * D * 2) + grp * 16384, &tmQ, q_full, w.h * a.G,
+                     w.q0 + w.tok0 + i * tt1, grp);
+        }
+        for (int n = 0; n < m && ok; ++n) {
+          const int pg_next = n + 1 < m ? pages_of(tile + n + 1) : -2;
+          if (NT == 1 && n + 1 < m) load_k(tile + n + 1, pg_next);
+          load_v(tile + n, pg);
+          if (NT == 2 && n + 1 < m) load_k(tile + n + 1, pg_next);
+          pg = pg_next;
+        }
+      }
+      w.next(a, c, m);
+    }
+    if (!ok && lane == 0) {
+      // every copy started is waited for (bounded) before the CTA can exit
+      for (int i = max(0, filled - NS); i < filled; ++i) mbar_wait(full0 + 8 * (i % NS), (i / NS) & 1);
+      if (q_count > 0) mbar_wait(q_full, (q_count - 1) & 1);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace fp8k

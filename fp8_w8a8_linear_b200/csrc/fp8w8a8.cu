@@ -231,6 +231,9 @@ fp8_status set_attn_attr(int sm_count, int* ctas) {
       n < 1)
     return FP8_ERR_CUDA;
   *ctas = n * sm_count;
+  if (cudaFuncSetAttribute(attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(ChunkCfg<D>::kSmem)) != cudaSuccess)
+    return FP8_ERR_CUDA;
   return FP8_OK;
 }
 
@@ -1544,18 +1547,23 @@ struct AttnWs {
   size_t total() const { return o + ml + desc; }
 };
 
+template <int D>
+AttnWs attn_ws_t(const DeviceInfo& dev) {
+  const size_t rows_ctas = dev.attn_rows_ctas[attn_width(D)], chunk_ctas = dev.sm_count;
+  const size_t rows = 2 * std::max(rows_ctas * kRowsMax, chunk_ctas * ChunkCfg<D>::kRows);
+  return {rows * D * 4, rows * 8, std::max(rows_ctas, chunk_ctas) * sizeof(int4)};
+}
+
 AttnWs attn_ws(const DeviceInfo& dev, int D) {
-  const size_t parts = 2 * static_cast<size_t>(dev.attn_rows_ctas[attn_width(D)]) * kRowsMax;
-  return {parts * D * 4, parts * 8, static_cast<size_t>(dev.attn_rows_ctas[attn_width(D)]) * sizeof(int4)};
+  return D == 64 ? attn_ws_t<64>(dev) : D == 128 ? attn_ws_t<128>(dev) : attn_ws_t<256>(dev);
 }
 
 // Map over one array of the paged cache for boxes of box_rows tokens of one
-// head of one page: [head_dim / 64][box_rows][64] bf16 with the 128-byte
-// swizzle (dimensions: 64 elements, token, group of 64, head, page). A size
+// head of one page: [groups][box_rows][64] bf16 with the 128-byte swizzle (dimensions: 64 elements, token, group of 64, head, page). A size
 // of one makes its stride meaningless; no page at all gets a map that no
 // load uses.
 bool make_tmap_paged(CUtensorMap* m, const uint16_t* base, const PagedArgs& c, int box_rows,
-                     const void* stand_in) {
+                     int groups, const void* stand_in) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const auto stride = [](int64_t n, int64_t st) { return static_cast<cuuint64_t>(n > 1 ? 2 * st : 128); };
@@ -1564,7 +1572,7 @@ bool make_tmap_paged(CUtensorMap* m, const uint16_t* base, const PagedArgs& c, i
                         static_cast<cuuint64_t>(c.heads), pages};
   cuuint64_t strides[4] = {stride(c.page_size, c.token_stride), 128, stride(c.heads, c.head_stride),
                            stride(c.num_pages, c.page_stride)};
-  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(c.D / 64), 1, 1};
+  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(groups), 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   std::memset(m, 0, sizeof(*m));
   void* p = c.num_pages > 0 ? const_cast<uint16_t*>(base) : const_cast<void*>(stand_in);
@@ -1580,13 +1588,39 @@ fp8_status launch_attn_rows(const DeviceInfo& dev, AttnArgs a, const PagedArgs& 
   const int ctas = dev.attn_rows_ctas[attn_width(D)];
   a.box_rows = std::min(kRowsBN, c.page_size & -c.page_size);
   CUtensorMap tmK, tmV;
-  if (!make_tmap_paged(&tmK, c.k, c, a.box_rows, a.q) || !make_tmap_paged(&tmV, c.v, c, a.box_rows, a.q))
+  if (!make_tmap_paged(&tmK, c.k, c, a.box_rows, D / 64, a.q) || !make_tmap_paged(&tmV, c.v, c, a.box_rows, D / 64, a.q))
     return FP8_ERR_CUDA;
   if (fp8_status st = launch_pdl_smem(attn_rows_kernel<D, S>, dim3(ctas), dim3(kRowsThreads),
                                       RowsCfg<D, S>::kSmem, stream, tmK, tmV, a, c))
     return st;
   const unsigned rows = static_cast<unsigned>(a.max_q * a.G);
   return launch_pdl(attn_join_kernel<D, kRowsMax, 8>, dim3(ctas, rows), dim3(256), stream, a);
+}
+
+// Items of up to two (head_dim 256: one) tiles of 128 rows, one CTA per SM,
+// then the join of what was cut.
+template <int D>
+fp8_status launch_attn_chunk(const DeviceInfo& dev, AttnArgs a, const PagedArgs& c, cudaStream_t stream) {
+  using C = ChunkCfg<D>;
+  a.box_rows = std::min(C::kVKeys, c.page_size & -c.page_size);
+  const int tt1 = 128 / a.G;
+  CUtensorMap tmQ, tmK, tmV;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return FP8_ERR_CUDA;
+  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.T), D / 64};
+  cuuint64_t strides[3] = {2 * D, 2 * static_cast<cuuint64_t>(a.ldq), 128};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(tt1), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  std::memset(&tmQ, 0, sizeof(tmQ));
+  if (fn(&tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(a.q), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+      !make_tmap_paged(&tmK, c.k, c, a.box_rows, 1, a.q) || !make_tmap_paged(&tmV, c.v, c, a.box_rows, 1, a.q))
+    return FP8_ERR_CUDA;
+  if (fp8_status st = launch_pdl_smem(attn_chunk_kernel<D>, dim3(dev.sm_count), dim3(C::kThreads), C::kSmem,
+                                      stream, tmQ, tmK, tmV, a, c))
+    return st;
+  return launch_pdl(attn_join_kernel<D, C::kRows, 1>, dim3(dev.sm_count, C::kRows / 8), dim3(256), stream, a);
 }
 
 }  // namespace
@@ -1637,7 +1671,7 @@ extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64
     if (c.D == 128) return launch_attn_rows<128>(*dev, a, c, as_stream(stream));
     return launch_attn_rows<256>(*dev, a, c, as_stream(stream));
   }
-  const dim3 grid(static_cast<unsigned>((T * q_heads + 3) / 4));
-  const auto kernel = c.D == 64 ? attn_simple_kernel<64> : c.D == 128 ? attn_simple_kernel<128> : attn_simple_kernel<256>;
-  return launch_pdl(kernel, grid, dim3(128), as_stream(stream), a, c);
+  if (c.D == 64) return launch_attn_chunk<64>(*dev, a, c, as_stream(stream));
+  if (c.D == 128) return launch_attn_chunk<128>(*dev, a, c, as_stream(stream));
+  return launch_attn_chunk<256>(*dev, a, c, as_stream(stream));
 }
