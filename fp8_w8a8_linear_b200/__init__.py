@@ -542,60 +542,65 @@ def cast_e4m3(x: torch.Tensor, out: torch.Tensor | None = None):
 _PAGED_KV = struct.Struct("@PP7qPqqPP")  # bf16_paged_kv
 
 
-def _on_current(t: torch.Tensor, dtype, name: str) -> torch.Tensor:
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+
+
+def _current(t: torch.Tensor, name: str):
+    """The current device and its current stream, once per call; t is the call's first tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _ptr(t: torch.Tensor, dtype, dev: int, name: str) -> int:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be a tensor on the current CUDA device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t
+    return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, name: str, shape=None):
-    """Address and token pitch of a bf16 [T, heads, head_dim] tensor whose heads lie side by side."""
-    _on_current(t, torch.bfloat16, name)
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must have shape {'[T, heads, head_dim]' if shape is None else tuple(shape)}, "
-                         f"got {tuple(t.shape)}")
+def _pitch(t: torch.Tensor, name: str) -> int:
+    """Token pitch of a [T, heads, head_dim] tensor whose heads lie side by side."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [T, heads, head_dim], got {tuple(t.shape)}")
     T, H, D = t.shape
     if t.is_contiguous():
-        return t.data_ptr(), H * D
+        return H * D
     st = t.stride()
     if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
         raise ValueError(f"{name}: the elements of a head and the heads of a token must lie side by side")
-    return t.data_ptr(), st[0] if T > 1 else H * D
+    return st[0] if T > 1 else H * D
 
 
-def _ints(t: torch.Tensor, name: str, n: int | None = None) -> int:
-    _on_current(t, torch.int32, name)
-    if not t.is_contiguous() or (n is not None and (t.dim() != 1 or t.shape[0] != n)):
-        raise ValueError(f"{name} must be contiguous" + ("" if n is None else f" with shape ({n},)"))
-    return t.data_ptr()
+def _vec(t: torch.Tensor, dtype, n: int, dev: int, name: str) -> int:
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape ({n},), got {tuple(t.shape)}")
+    return _ptr(t, dtype, dev, name)
 
 
-def _frequencies(t: torch.Tensor, name: str) -> int:
-    _on_current(t, torch.float32, name)
-    if t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector")
-    return t.data_ptr()
+def _same(t: torch.Tensor, shape, name: str):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, head_dim):
-    _on_current(k_cache, torch.bfloat16, "k_cache")
-    _on_current(v_cache, torch.bfloat16, "v_cache")
+def _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, head_dim: int, dev: int):
     if k_cache.dim() != 4 or k_cache.shape[3] != head_dim:
         raise ValueError(f"k_cache must be [pages, page_size, heads, {head_dim}], got {tuple(k_cache.shape)}")
-    pages, page_size, heads, _ = k_cache.shape
+    pages, page_size, heads, _ = shape = k_cache.shape
     st = k_cache.stride()
-    if v_cache.shape != k_cache.shape or v_cache.stride() != st:
+    if v_cache.shape != shape or v_cache.stride() != st:
         raise ValueError("v_cache must have the shape and strides of k_cache")
     if st[3] != 1:
         raise ValueError("k_cache: the elements of a head must lie side by side")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [batch, max_pages]")
+    if page_table.dim() != 2 or not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous [batch, max_pages] tensor")
     batch, max_pages = page_table.shape
-    return _PAGED_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), pages, page_size, heads, head_dim, st[0], st[1],
-                          st[2], _ints(page_table, "page_table"), batch, max_pages, _ints(cu_q, "cu_q", batch + 1),
-                          _ints(kv_lens, "kv_lens", batch))
+    return _PAGED_KV.pack(_ptr(k_cache, _BF16, dev, "k_cache"), _ptr(v_cache, _BF16, dev, "v_cache"), pages, page_size,
+                          heads, head_dim, st[0], st[1], st[2], _ptr(page_table, _I32, dev, "page_table"), batch,
+                          max_pages, _vec(cu_q, _I32, batch + 1, dev, "cu_q"),
+                          _vec(kv_lens, _I32, batch, dev, "kv_lens"))
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -638,12 +643,18 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, inter
          amplitude: float = 1.0, y: torch.Tensor | None = None):
     """x bf16 [T, heads, head_dim] with the first 2 * len(inv_freq) elements of each head turned by positions int32 [T]
     (y may be x)."""
-    xp, ldx = _heads(x, "x")
-    T, H, D = x.shape
-    y = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device) if y is None else y
-    yp, ldy = _heads(y, "y", x.shape)
-    _check(_lib.bf16_rope(xp, ldx, _ints(positions, "positions", T), _frequencies(inv_freq, "inv_freq"), T, H, D,
-                          2 * inv_freq.shape[0], interleaved, amplitude, yp, ldy, _stream()), "bf16_rope")
+    dev, stream = _current(x, "x")
+    ldx = _pitch(x, "x")
+    T, H, D = shape = x.shape
+    if y is None:
+        y, ldy = x.new_empty(shape), H * D
+    else:
+        _same(y, shape, "y")
+        ldy = _pitch(y, "y")
+    R = inv_freq.numel()
+    _check(_lib.bf16_rope(_ptr(x, _BF16, dev, "x"), ldx, _vec(positions, _I32, T, dev, "positions"),
+                          _vec(inv_freq, _F32, R, dev, "inv_freq"), T, H, D, 2 * R, interleaved, amplitude,
+                          _ptr(y, _BF16, dev, "y"), ldy, stream), "bf16_rope")
     return y
 
 
@@ -655,27 +666,33 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     head_dim], any strides for the first three), the keys turned by their positions when inv_freq is given. With q
     [T, q_heads, head_dim] the queries are turned too, into q_out (new when None; may be q), which is returned.
     page_table int32 [batch, max_pages], cu_q int32 [batch + 1], kv_lens int32 [batch] (the new tokens counted)."""
-    kp, ldk = _heads(k, "k")
-    T, H, D = k.shape
-    vp, ldv = _heads(v, "v", k.shape)
-    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, D)
+    dev, stream = _current(k, "k")
+    ldk, ldv = _pitch(k, "k"), _pitch(v, "v")
+    T, H, D = shape = k.shape
+    _same(v, shape, "v")
+    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, D, dev)
     if k_cache.shape[2] != H:
         raise ValueError(f"k has {H} heads, the cache {k_cache.shape[2]}")
-    qp = qop = None
-    ldq = ldqo = Hq = 0
+    qp = qop = fp = None
+    ldq = ldqo = Hq = R = 0
     if q is not None:
-        qp, ldq = _heads(q, "q")
+        ldq = _pitch(q, "q")
         Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != D:
-            raise ValueError(f"q must have shape ({T}, q_heads, {D}), got {tuple(q.shape)}")
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
-        qop, ldqo = _heads(q_out, "q_out", q.shape)
+        _same(q, (T, Hq, D), "q")
+        qp = _ptr(q, _BF16, dev, "q")
+        if q_out is None:
+            q_out, ldqo = q.new_empty((T, Hq, D)), Hq * D
+        else:
+            _same(q_out, (T, Hq, D), "q_out")
+            ldqo = _pitch(q_out, "q_out")
+        qop = _ptr(q_out, _BF16, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out is given without q")
-    R = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    _check(_lib.bf16_kv_append(kp, ldk, vp, ldv, qp, ldq, qop, ldqo, Hq, T, kv,
-                               None if inv_freq is None else _frequencies(inv_freq, "inv_freq"), R, interleaved,
-                               amplitude, _stream()), "bf16_kv_append")
+    if inv_freq is not None:
+        R = inv_freq.numel()
+        fp = _vec(inv_freq, _F32, R, dev, "inv_freq")
+    _check(_lib.bf16_kv_append(_ptr(k, _BF16, dev, "k"), ldk, _ptr(v, _BF16, dev, "v"), ldv, qp, ldq, qop, ldqo, Hq, T, kv,
+                               fp, 2 * R, interleaved, amplitude, stream), "bf16_kv_append")
     return q_out
 
 
@@ -693,23 +710,27 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     last ``window`` keys when window > 0; scale defaults to head_dim^-0.5. max_q: no sequence has more new tokens
     (None: T). lse fp32 [T, q_heads] receives ln sum exp of the scores when given. Returns out bf16 [T, q_heads,
     head_dim]; rows behind cu_q[batch] stay as they are."""
-    qp, ldq = _heads(q, "q")
-    T, Hq, D = q.shape
-    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, D)
-    out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-    op, ldo = _heads(out, "out", q.shape)
+    dev, stream = _current(q, "q")
+    ldq = _pitch(q, "q")
+    T, Hq, D = shape = q.shape
+    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, D, dev)
+    if out is None:
+        out, ldo = q.new_empty(shape), Hq * D
+    else:
+        _same(out, shape, "out")
+        ldo = _pitch(out, "out")
     lp = None
     if lse is not None:
-        _on_current(lse, torch.float32, "lse")
         if lse.shape != (T, Hq) or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous with shape ({T}, {Hq})")
-        lp = lse.data_ptr()
-    ws = paged_attention_workspace(D) if ws is None else _on_current(ws, torch.uint8, "ws")
-    if not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
-    _check(_lib.bf16_paged_attention(qp, ldq, T, Hq, kv, 0 if max_q is None else max_q,
-                                     D ** -0.5 if scale is None else scale, window, op, ldo, lp, ws.data_ptr(),
-                                     ws.numel(), _stream()), "bf16_paged_attention")
+        lp = _ptr(lse, _F32, dev, "lse")
+    if ws is None:
+        ws = paged_attention_workspace(D)
+    elif ws.dim() != 1 or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous vector of bytes")
+    _check(_lib.bf16_paged_attention(_ptr(q, _BF16, dev, "q"), ldq, T, Hq, kv, 0 if max_q is None else max_q,
+                                     D ** -0.5 if scale is None else scale, window, _ptr(out, _BF16, dev, "out"), ldo,
+                                     lp, _ptr(ws, _U8, dev, "ws"), ws.shape[0], stream), "bf16_paged_attention")
     return out
 
 
