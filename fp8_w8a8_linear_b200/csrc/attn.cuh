@@ -65,20 +65,27 @@ __device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, const PagedArgs& 
   s.len = c.kv_lens[b];
   s.ok = seq_ok(c, s.q0, q1, s.len, a.T) && q1 - s.q0 <= a.max_q;
   s.ql = s.ok ? q1 - s.q0 : 0;
-  s.lo = static_cast<int>(max(0ll, static_cast<long long>(s.len) - s.ql - a.window + 1));
+  s.lo = max(0, s.len - s.ql - a.window + 1);  // lengths and window are at most 2^30
   s.tile0 = s.lo / BN;
   s.tiles = s.ql == 0 ? 0 : max(1, (s.len + BN - 1) / BN - s.tile0);
   return s;
 }
 
-// A CTA's run: `units` key tiles from tile `tile` of the item (seq, sub) on
-// (sub numbers a sequence's items); `per` is the length of a full run.
+// A CTA's run: `units` key tiles from one of sequence `seq`'s on; `per` is
+// the length of a full run.
 struct AttnRun {
   int seq;
   int units;
   int per;
-  long long sub_off;  // units of the sequence before the run
+  int head, block, tile;  // where in the sequence it starts
+  long long sub_off;      // units of the sequence before it
 };
+
+// Quotients of numbers that nearly always fit 32 bits (a 64-bit division
+// takes some hundred cycles).
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
 
 template <int THREADS>
 struct PlanSmem {
@@ -104,7 +111,7 @@ __device__ __forceinline__ AttnRun find_run(PlanSmem<THREADS>& sm, int batch, in
   long long total = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) total += sm.wsum[i];
-  const long long per = max(1ll, (total + ctas - 1) / ctas);
+  const long long per = max(1ll, div_ll(total + ctas - 1, ctas));
   const long long start = per * cta;
   if (start < total) {  // block-uniform
     long long base = 0;
@@ -147,6 +154,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+constexpr int kRowsMax = 16;  // rows of an attn_rows_kernel item
 constexpr float kLn2 = 0.69314718055994531f;
 
 // ------------------------------------------------------------------ join
@@ -157,47 +165,41 @@ __device__ __forceinline__ int4 join_desc(int more, int slot, int t0, int h0, in
   return make_int4(more | (rows << 16), slot, t0, h0);
 }
 
-// One block per (CTA that holds an item's first part, row group): a row by
-// WPR warps, each adding the parts w, w + WPR, ..., joined in warp order.
-template <int D, int ROWS, int WPR>
-__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a) {
+// Parts of attn_rows_kernel, [slot][row][D]. One block per row of an item:
+// warp w adds the parts w, w + 8, ... (a single long context has hundreds),
+// then the warps' sums are added in order.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_rows_kernel(AttnArgs a) {
   constexpr int E = D / 32;  // values per lane
-  constexpr int RPB = 8 / WPR;
-  __shared__ float so[WPR > 1 ? 8 : 1][D];
+  __shared__ float so[8][D];
   pdl_launch_dependents();
   pdl_wait();
   const int4 d = a.part_desc[blockIdx.x];
-  const int more = d.x & 0xFFFF, rows = d.x >> 16;
-  if (more == 0) return;
+  const int more = d.x & 0xFFFF, rows = d.x >> 16, r = blockIdx.y;
+  if (more == 0 || r >= rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * RPB + warp / WPR, w = warp % WPR;
-  if (WPR == 1 ? r >= rows : blockIdx.y * RPB >= rows) return;
-  auto slot = [&](int i) { return i == 0 ? d.y : 2 * (static_cast<int>(blockIdx.x) + i); };
-  const bool live = r < rows;
-  // every part's maximum and sum, by all lanes (each warp of the row alike)
+  const auto slot = [&](int i) { return i == 0 ? d.y : 2 * (static_cast<int>(blockIdx.x) + i); };
+  // every part's maximum and sum, by all lanes (each warp alike)
   float m = -INFINITY;
-  for (int i = lane; live && i <= more; i += 32)
-    m = fmaxf(m, a.part_ml[static_cast<int64_t>(slot(i)) * ROWS + r].x);
+  for (int i = lane; i <= more; i += 32) m = fmaxf(m, a.part_ml[static_cast<int64_t>(slot(i)) * kRowsMax + r].x);
 #pragma unroll
   for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
   const float mb = m == -INFINITY ? 0.0f : m;
   float l = 0.0f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  for (int i0 = 0; live && i0 <= more; i0 += 32) {
+  for (int i0 = 0; i0 <= more; i0 += 32) {
     float f_l = 0.0f;
     if (i0 + lane <= more) {
-      const float2 ml = a.part_ml[static_cast<int64_t>(slot(i0 + lane)) * ROWS + r];
+      const float2 ml = a.part_ml[static_cast<int64_t>(slot(i0 + lane)) * kRowsMax + r];
       f_l = ex2(ml.x - mb);
       l += f_l * ml.y;
     }
     const int n = min(32, more + 1 - i0);
-    const int first = (w - i0 % WPR + WPR) % WPR;
 #pragma unroll 4
-    for (int i = first; i < n; i += WPR) {
+    for (int i = warp; i < n; i += 8) {
       const float f = __shfl_sync(0xFFFFFFFFu, f_l, i);
-      if (f == 0.0f) continue;  // a part in which the row saw no key may have no o
-      const float* p = a.part_o + (static_cast<int64_t>(slot(i0 + i)) * ROWS + r) * D + lane * (E < 4 ? E : 4);
+      const float* p = a.part_o + (static_cast<int64_t>(slot(i0 + i)) * kRowsMax + r) * D + lane * (E < 4 ? E : 4);
       if constexpr (E == 2) {
         const float2 v = *reinterpret_cast<const float2*>(p);
         acc[0] += f * v.x, acc[1] += f * v.y;
@@ -212,15 +214,13 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a) {
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, s);
-  if constexpr (WPR > 1) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
-    __syncthreads();
-    if (w != 0 || !live) return;
-    for (int i = 1; i < WPR; ++i)
+  for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
+  __syncthreads();
+  if (warp != 0) return;
+  for (int i = 1; i < 8; ++i)
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += so[warp + i][lane * E + e];
-  }
+    for (int e = 0; e < E; ++e) acc[e] += so[i][lane * E + e];
   const int t = d.z + r / a.G, h = d.w + r % a.G;
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   uint16_t* o = a.o + t * a.ldo + static_cast<int64_t>(h) * D + lane * (E < 4 ? E : 4);
@@ -237,6 +237,58 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a) {
     a.lse[static_cast<int64_t>(t) * a.Hq + h] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
+// Parts of attn_chunk_kernel, [slot][D / 4][row][4]: written by one thread
+// per row, so that a warp's store is 512 bytes in a row. One block per 32
+// rows of an item: a lane per row, the columns dealt to the eight warps; the
+// rows leave through shared memory, 16 bytes a lane.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) attn_join_chunk_kernel(AttnArgs a) {
+  constexpr int Q = D / 32;  // groups of four columns per warp
+  __shared__ __align__(16) uint16_t so[32][D + 8];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int4 d = a.part_desc[blockIdx.x];
+  const int more = d.x & 0xFFFF, rows = d.x >> 16;
+  if (more == 0 || static_cast<int>(blockIdx.y) * 32 >= rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * 32 + lane;
+  const bool live = r < rows;
+  const auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? d.y : 2 * (static_cast<int>(blockIdx.x) + i)); };
+  float m = -INFINITY, l = 0.0f;
+  for (int i = 0; live && i <= more; ++i) m = fmaxf(m, a.part_ml[slot(i) * ROWS + r].x);
+  const float mb = m == -INFINITY ? 0.0f : m;
+  float4 acc[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) acc[q] = make_float4(0, 0, 0, 0);
+  for (int i = 0; live && i <= more; ++i) {
+    const float2 ml = a.part_ml[slot(i) * ROWS + r];
+    const float f = ex2(ml.x - mb);
+    l += f * ml.y;
+    if (f == 0.0f) continue;  // a part in which the row saw no key has no o
+    const float4* p = reinterpret_cast<const float4*>(a.part_o) + slot(i) * (D / 4) * ROWS + r;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const float4 v = p[(warp + 8 * q) * ROWS];
+      acc[q].x += f * v.x, acc[q].y += f * v.y, acc[q].z += f * v.z, acc[q].w += f * v.w;
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    *reinterpret_cast<uint2*>(&so[lane][4 * (warp + 8 * q)]) =
+        make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
+  if (a.lse && live && warp == 0)
+    a.lse[static_cast<int64_t>(d.z + r / a.G) * a.Hq + d.w + r % a.G] =
+        l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * (D / 8); i += 256) {
+    const int rr = i / (D / 8), c8 = i % (D / 8), ro = blockIdx.y * 32 + rr;
+    if (ro < rows)
+      *reinterpret_cast<uint4*>(a.o + (d.z + ro / a.G) * a.ldo + static_cast<int64_t>(d.w + ro % a.G) * D + 8 * c8) =
+          *reinterpret_cast<const uint4*>(&so[rr][8 * c8]);
+  }
+}
+
 // ------------------------------------------------------------------ few rows
 // attn_rows_kernel: items of at most 16 rows (one or a few new tokens times
 // the heads of a group). Bound by the cache's bytes: 16 rows are 16 flops a
@@ -248,7 +300,6 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a) {
 // the main loop has no exchange between warps; they join through shared
 // memory at an item's end.
 constexpr int kRowsBN = 64;
-constexpr int kRowsMax = 16;
 constexpr int kRowsThreads = 160;
 
 template <int D, int SLOTS>
@@ -304,8 +355,8 @@ struct RowsWalk {
     h = 0, t = 0;
     if (left > 0) {
       s = seq_span(a, c, b, kRowsBN);
-      h = static_cast<int>(r.sub_off / s.tiles);
-      t = static_cast<int>(r.sub_off % s.tiles);
+      h = static_cast<int>(div_ll(r.sub_off, s.tiles));
+      t = static_cast<int>(r.sub_off - static_cast<long long>(h) * s.tiles);
     }
   }
   __device__ __forceinline__ int seg() const { return min(left, s.tiles - t); }
@@ -644,24 +695,25 @@ struct ChunkCfg {
   static constexpr int kKCols = D < 128 ? D : 128;   // head elements of a key slot
   static constexpr int kVKeys = kChunkBN / kParts;   // keys of a value slot
   static constexpr int kQBytes = kNT * 128 * D * 2;
-  static constexpr int kThreads = kNT * 128 + 64;
+  static constexpr int kThreads = kNT * 128 + 128;
   static constexpr int kRows = kNT * 128;            // rows of a part in the workspace
   static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kSlots) * kSlotBytes +
                                   8 * (2 * kSlots + 10) + 32 + sizeof(PlanSmem<kThreads>);
 };
 
-// sum_{i < n} floor((a i + b) / m), a, b >= 0 (the Euclid-like recursion on
-// lattice points under a line).
-__device__ __forceinline__ long long floor_sum(long long n, uint32_t m, uint32_t a, long long b) {
+// sum_{i < n} floor((a i + b) / m) for a n + b < 2^32 (the Euclid-like
+// recursion on lattice points under a line).
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long s = 0;
   while (n > 0) {
-    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long y = a * n + b;
+    const uint32_t qa = a / m, qb = b / m;
+    s += static_cast<long long>(n) * (n - 1) / 2 * qa + static_cast<long long>(n) * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
-    b = y % m;
+    b = y - n * m;
     const uint32_t t = m;
     m = a;
     a = t;
@@ -669,21 +721,77 @@ __device__ __forceinline__ long long floor_sum(long long n, uint32_t m, uint32_t
   return s;
 }
 
-// Key tiles of a sequence's first j blocks of tt new tokens (nb blocks in
-// all; first = the first new token's position). Block i sees the keys from
-// max(0, first + i tt - window + 1) to its last token, in tiles of 128, and
-// takes one tile where it sees none.
-__device__ __forceinline__ long long chunk_prefix(int first, int len, int window, int tt, int nb, int j) {
-  if (len == 0 || j == 0) return j;
-  const long long f = first;
-  const int je = f < 0 ? static_cast<int>(min(static_cast<long long>(j), -f / tt)) : 0;
-  const bool last = j == nb;  // the last block ends at len
-  long long s = je + floor_sum(j - (last ? 1 : 0) - je, kChunkBN, tt, f + (je + 1ll) * tt + kChunkBN - 1);
-  if (last) s += (len + static_cast<long long>(kChunkBN) - 1) / kChunkBN;
-  const long long x = window - 1 - f;
-  const long long jw = max(static_cast<long long>(je), x < 0 ? 0ll : x / tt + 1);
-  if (j > jw) s -= floor_sum(j - jw, kChunkBN, tt, f + jw * tt - window + 1);
+// Key tiles that block j (tt tokens from tok0 on, the first at position
+// first + tok0) of a sequence sees: from max(0, p - window + 1) to its last
+// token, in tiles of 128; one where it sees none.
+__device__ __forceinline__ int block_tiles(int first, int window, int tok0, int ntok, int& tile0) {
+  const int p0 = first + tok0;
+  tile0 = max(0, p0 < window ? 0 : p0 - window + 1) / kChunkBN;
+  return max(1, (max(0, p0 + ntok) + kChunkBN - 1) / kChunkBN - tile0);
+}
+
+// The sum of block_tiles over a sequence's nb blocks of tt tokens.
+__device__ __forceinline__ long long chunk_tiles(int first, int len, int window, int tt, int ql) {
+  const int nb = (ql + tt - 1) / tt;
+  if (nb <= 8) {
+    long long s = 0;
+    int tile0;
+    for (int j = 0; j < nb; ++j) s += block_tiles(first, window, j * tt, min(tt, ql - j * tt), tile0);
+    return s;
+  }
+  if (len == 0) return nb;
+  const int je = first < 0 ? -first / tt : 0;  // blocks before position 0, one tile each
+  long long s = je + (len + kChunkBN - 1) / kChunkBN +
+                floor_sum(nb - 1 - je, kChunkBN, tt, first + (je + 1) * tt + kChunkBN - 1);
+  const int x = first >= window ? -1 : window - 1 - first;
+  const int jw = max(je, x < 0 ? 0 : x / tt + 1);  // first block that starts past tile 0's first key
+  if (nb > jw) s -= floor_sum(nb - jw, kChunkBN, tt, first + jw * tt - window + 1);
   return s;
+}
+
+// Finds the head, block and tile at which a run starts in its sequence (the
+// whole block calls it): the blocks' tiles are added up a block per thread.
+template <int THREADS>
+__device__ __forceinline__ void find_block(PlanSmem<THREADS>& sm, AttnRun& r, const AttnArgs& a,
+                                           const PagedArgs& c, int tt) {
+  constexpr int W = THREADS / 32;
+  if (r.units <= 0) return;  // block-uniform
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const SeqSpan s = seq_span(a, c, r.seq, kChunkBN);
+  const int first = s.len - s.ql, nb = (s.ql + tt - 1) / tt;
+  const long long per_head = chunk_tiles(first, s.len, a.window, tt, s.ql);
+  r.head = static_cast<int>(div_ll(r.sub_off, per_head));
+  const long long off = r.sub_off - r.head * per_head;
+  long long base = 0;
+  for (int j0 = 0; j0 < nb && base <= off; j0 += THREADS) {
+    const int j = j0 + tid;
+    int tile0;
+    const int mine = j < nb ? block_tiles(first, a.window, j * tt, min(tt, s.ql - j * tt), tile0) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    __syncthreads();  // wsum is free
+    if (lane == 31) sm.wsum[w] = incl;
+    __syncthreads();
+    long long before = base, all = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      before += i < w ? sm.wsum[i] : 0;
+      all += sm.wsum[i];
+    }
+    const long long hi = before + incl, lo = hi - mine;
+    if (lo <= off && off < hi) {
+      sm.run.block = j;
+      sm.run.tile = static_cast<int>(off - lo);
+    }
+    base += all;
+  }
+  __syncthreads();
+  r.block = sm.run.block;
+  r.tile = sm.run.tile;
 }
 
 // A run's segments: tiles t .. of item (sequence b, head h, block j).
@@ -705,33 +813,13 @@ struct ChunkWalk {
   __device__ __forceinline__ void item(const AttnArgs& a) {
     tok0 = j * tt;
     ntok = min(ql - tok0, tt);
-    const long long p0 = static_cast<long long>(first) + tok0;
-    const int lo = static_cast<int>(max(0ll, p0 - a.window + 1));
-    const int hi = max(0, first + tok0 + ntok);
-    tile0 = lo / kChunkBN;
-    n = max(1, (hi + kChunkBN - 1) / kChunkBN - tile0);
+    n = block_tiles(first, a.window, tok0, ntok, tile0);
   }
-  // Whole warps call it (the search for the block uses the lanes).
   __device__ __forceinline__ ChunkWalk(const AttnArgs& a, const PagedArgs& c, const AttnRun& r, int tt_) {
     tt = tt_;
-    b = r.seq, left = r.units, h = 0, j = 0, t = 0;
+    b = r.seq, left = r.units, h = r.head, j = r.block, t = r.tile;
     if (left <= 0) return;
     seq(a, c);
-    const long long per_head = chunk_prefix(first, len, a.window, tt, nb, nb);
-    h = static_cast<int>(r.sub_off / per_head);
-    const long long off = r.sub_off % per_head;
-    // the last block whose tiles start at or before off: 32 probes a round
-    int lo = 0, hi = nb;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32;
-      const int probe = lo + step * static_cast<int>(lane_id());
-      const bool le = probe < hi && chunk_prefix(first, len, a.window, tt, nb, probe) <= off;
-      const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, le));  // lane 0's probe is lo: always at or below
-      lo += step * k;
-      hi = min(hi, lo + step);
-    }
-    j = lo;
-    t = static_cast<int>(off - chunk_prefix(first, len, a.window, tt, nb, j));
     item(a);
   }
   __device__ __forceinline__ int seg() const { return min(left, n - t); }
@@ -761,7 +849,7 @@ struct ChunkWalk {
     from = to = 0;
     if (nt == 0) return;
     const int p0 = first + tok0 + i * tt1;
-    const int lo = static_cast<int>(max(0ll, static_cast<long long>(p0) - a.window + 1)) / kChunkBN;
+    const int lo = (p0 < a.window ? 0 : p0 - a.window + 1) / kChunkBN;
     const int hi = max(lo + 1, (max(0, p0 + nt) + kChunkBN - 1) / kChunkBN);
     from = max(0, lo - tile0 - t);
     to = min(m, hi - tile0 - t);
@@ -792,18 +880,18 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Descriptor of an operand tile whose contiguous dimension is M/N (not K),
-// written by TMA with the 128-byte swizzle: 64 elements of M/N by eight of K
-// make a 1024-byte atom; lead_bytes from one group of 64 to the next, 1024
-// from eight of K to the next eight.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t lead_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((lead_bytes >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
+// Shared-memory descriptors by halves: the upper one is the same for all
+// operands here (1024 bytes from eight rows, or eight of K, to the next;
+// version 1; 128-byte swizzle), the lower one is the address in 16-byte
+// units, to which offsets are simply added, and the lead offset: unused
+// where K is contiguous, and where M/N is (the values: 64 elements of N by
+// eight keys make a 1024-byte atom) the bytes from one group of 64 to the next.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t lead_bytes) {
+  return (smem_addr >> 4) | (lead_bytes >> 4 << 16);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  return (static_cast<uint64_t>(kDescHi) << 32) | lo;
 }
 constexpr uint32_t kIdescBMnMajor = 1u << 16;  // operand B's contiguous dimension is N
 
@@ -828,6 +916,31 @@ __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map,
       : "memory");
 }
 
+// A warpgroup's share of the block's registers (whole warpgroups call it).
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The largest of three (one instruction).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two sums, packed.
+__device__ __forceinline__ void fadd2(float2& s, float a, float b) {
+  asm("{\n\t.reg .b64 ps, pa;\n\t"
+      "mov.b64 ps, {%0, %1};\n\tmov.b64 pa, {%2, %3};\n\t"
+      "add.rn.f32x2 ps, ps, pa;\n\tmov.b64 {%0, %1}, ps;\n\t}"
+      : "+f"(s.x), "+f"(s.y)
+      : "f"(a), "f"(b));
+}
+
 // Two products plus a shared pair: d = a * b + c per lane.
 __device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b, float c) {
   asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\t"
@@ -835,6 +948,24 @@ __device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, 
       "fma.rn.f32x2 pd, pa, pb, pc;\n\tmov.b64 {%0, %1}, pd;\n\t}"
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+// u[j] of lane q of four becomes u[q] of lane j: 4 x 4 pieces of 16 bytes.
+__device__ __forceinline__ void quad_transpose(uint32_t (&u)[4][4], int lane) {
+#pragma unroll
+  for (int s = 1; s <= 2; s <<= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & s) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t r = __shfl_xor_sync(0xFFFFFFFFu, up ? u[j][e] : u[j + s][e], s);
+        u[j][e] = up ? r : u[j][e];
+        u[j + s][e] = up ? u[j + s][e] : r;
+      }
+    }
+  }
 }
 
 // The softmax of one row tile's rows, one thread per row.
@@ -884,9 +1015,10 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
       float mx[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        mx[q] = __uint_as_float(s[q][0]);
+        mx[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
 #pragma unroll
-        for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][e]));
+        for (int e = 2; e < 32; e += 2)
+          mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
       }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
       const bool grow = top > mu + 8.0f;
@@ -911,7 +1043,7 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
         }
       }
       const float shift = mu == -INFINITY ? 0.0f : -mu;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float2 sum[2] = {};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t pk[16];
@@ -921,12 +1053,12 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
           ffma2(x0, x1, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]), a.scale_log2, shift);
           x0 = ex2(x0);
           x1 = ex2(x1);
-          sum[q] += x0 + x1;
+          fadd2(sum[q & 1], x0, x1);
           pk[e / 2] = pack_bf16x2(x0, x1);
         }
         tmem_st16(s_addr + 16 * q, pk);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -949,26 +1081,41 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
       if (!ok) break;
       tc_fence_after();
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      if (whole) {
+        // Four lanes turn their rows' 16-byte pieces among themselves, so that
+        // a store covers 8 rows x 64 bytes instead of 32 x 16.
+        const int64_t mine = live ? tok * a.ldo + static_cast<int64_t>(head) * D : -1;
+        int64_t at[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) at[j] = __shfl_sync(0xFFFFFFFFu, mine, (lane & ~3) + j);
 #pragma unroll 1
-      for (int cb = 0; cb < D; cb += 32) {
-        uint32_t o[32];
-        tmem_ld32(o_addr + cb, o);
-        tmem_ld_wait();
-        if (live && whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.o + tok * a.ldo + static_cast<int64_t>(head) * D + cb);
+        for (int cb = 0; cb < D; cb += 32) {
+          uint32_t o[32], u[4][4];
+          tmem_ld32(o_addr + cb, o);
+          tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v[8];
+          for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * q + e]) * inv;
-            dst[q] = f32_to_bf16x8(v);
-          }
-        } else if (live) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(part) * C::kRows + row) * D + cb);
+            for (int e = 0; e < 4; ++e)
+              u[q][e] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
+          quad_transpose(u, lane);
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
-                                 __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+          for (int j = 0; j < 4; ++j)
+            if (at[j] >= 0)
+              *reinterpret_cast<uint4*>(a.o + at[j] + cb + 8 * (lane & 3)) = make_uint4(u[j][0], u[j][1], u[j][2], u[j][3]);
+        }
+      } else {
+        float4* dst = reinterpret_cast<float4*>(a.part_o) + static_cast<int64_t>(part) * (D / 4) * C::kRows + row;
+#pragma unroll 1
+        for (int cb = 0; cb < D; cb += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + cb, o);
+          tmem_ld_wait();
+          if (live)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[(cb / 4 + q) * C::kRows] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                                         __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
         }
       }
       tc_fence_before();
@@ -1005,7 +1152,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   auto* plan = reinterpret_cast<PlanSmem<C::kThreads>*>(words + 8);
   const uint32_t q_smem = smem_u32(smem), slot0 = smem_u32(slots);
   const int warp = warp_id(), lane = lane_id();
-  constexpr int kMmaWarp = NT * 4, kLoadWarp = NT * 4 + 1;
+  constexpr int kMmaWarp = NT * 4, kLoadWarp = NT * 4 + 1;  // and kLoadWarp + 1
 
   if (threadIdx.x == 0) {
     st_shared_volatile_u32(abort_w, 0u);
@@ -1037,22 +1184,29 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   pdl_launch_dependents();  // this CTA holds its TMEM
   pdl_wait();
   const int tt1 = 128 / a.G, tt = NT * tt1;
-  const AttnRun run = find_run<C::kThreads>(*plan, c.batch, blockIdx.x, gridDim.x, [&](int b) -> long long {
+  AttnRun run = find_run<C::kThreads>(*plan, c.batch, blockIdx.x, gridDim.x, [&](int b) -> long long {
     const SeqSpan s = seq_span(a, c, b, kChunkBN);
     if (!s.ok && blockIdx.x == 0) report(FP8_DEV_BAD_INDEX);
     if (s.ql == 0) return 0;
-    const int nb = (s.ql + tt - 1) / tt;
-    return chunk_prefix(s.len - s.ql, s.len, a.window, tt, nb, nb) * c.heads;
+    return chunk_tiles(s.len - s.ql, s.len, a.window, tt, s.ql) * c.heads;
   });
+  find_block(*plan, run, a, c, tt);
   ChunkWalk w(a, c, run, tt);
 
+  // Two row tiles: 384 threads of 168 registers at launch; the softmax keeps
+  // a row's 128 scores in registers, so its warps take 216 and the issuing
+  // ones 72 (2 x 128 x 216 + 128 x 72 = 384 x 168). One row tile: 256
+  // threads have 255 each as it is.
   if (warp < kMmaWarp) {
+    if constexpr (NT == 2) regs_inc<216>();
     const int tile = warp >> 2;
     chunk_softmax<D>(a, c, w, tile, tt1, tmem, s_full, p_full, o_done + 8 * tile, abort_w, run.per);
   } else if (warp == kMmaWarp) {
+    if constexpr (NT == 2) regs_dec<72>();
     // ------------------------------------------------------------- MMA issue
     constexpr uint32_t kIdescS = idesc_kind<kKindBF16>(128, kChunkBN);
     constexpr uint32_t kIdescO = idesc_kind<kKindBF16>(128, D) | kIdescBMnMajor;
+    const uint32_t q_lo = desc_lo(q_smem, 16), k_lo = desc_lo(slot0, 16), v_lo = desc_lo(slot0, C::kVKeys * 128);
     int slot = 0;            // next slot in load order
     uint32_t phase = 0;
     uint32_t q_count = 0, p_count[2] = {0, 0};
@@ -1082,12 +1236,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const auto scores = [&](int tile, int buf, const int (&at)[PARTS]) {
       if (ok && lane == 0) {
         tc_fence_after();
+        uint32_t kb[PARTS];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) kb[p] = k_lo + at[p] * (C::kSlotBytes / 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t qa = q_smem + tile * (128 * D * 2) + (k >> 2) * 16384 + (k & 3) * 32;
           const int p = k * 16 / C::kKCols, kk = k - p * (C::kKCols / 16);
-          const uint32_t kb = slot0 + at[p] * C::kSlotBytes + (kk >> 2) * 16384 + (kk & 3) * 32;
-          umma_kind<kKindBF16>(tmem + 128 * buf, sw128_kmajor_desc(qa), sw128_kmajor_desc(kb), kIdescS, k > 0);
+          umma_kind<kKindBF16>(tmem + 128 * buf,
+                               desc_of(q_lo + (tile * (128 * D * 2) + (k >> 2) * 16384 + (k & 3) * 32) / 16),
+                               desc_of(kb[p] + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16), kIdescS, k > 0);
         }
         umma_commit(s_full + 8 * buf);
       }
@@ -1096,12 +1253,14 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const auto product = [&](int tile, int buf, const int (&at)[PARTS], bool add) {
       if (ok && lane == 0) {
         tc_fence_after();
+        uint32_t vb[PARTS];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) vb[p] = v_lo + at[p] * (C::kSlotBytes / 16);
 #pragma unroll
         for (int k = 0; k < kChunkBN / 16; ++k) {
           const int p = k * 16 / C::kVKeys, kk = k - p * (C::kVKeys / 16);
-          umma_bf16_ts(tmem + 256 + tile * D, tmem + 128 * buf + 8 * k,
-                       sw128_mnmajor_desc(slot0 + at[p] * C::kSlotBytes + kk * 2048, C::kVKeys * 128), kIdescO,
-                       add || k > 0);
+          umma_bf16_ts(tmem + 256 + tile * D, tmem + 128 * buf + 8 * k, desc_of(vb[p] + kk * 2048 / 16), kIdescO,
+                       k > 0 ? 1u : static_cast<uint32_t>(add));
         }
         umma_commit(o_done + 8 * tile);
       }
@@ -1183,80 +1342,109 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       umma_commit(drained);
       mbar_wait(drained, 0);
     }
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    if constexpr (NT == 2) regs_dec<72>();
     // ------------------------------------------------------------- loads
+    // One warp for queries and keys, one for values; they share the ring,
+    // whose order both know, and each passes over the other's slots.
+    const bool keys = warp == kLoadWarp;
+    const CUtensorMap* map = keys ? &tmK : &tmV;
     const int rows = a.box_rows;
     constexpr int kColGroups = C::kKCols / 64, kAllGroups = D / 64;
     const uint32_t box_bytes = static_cast<uint32_t>(rows) * 128;
+    // a slot's boxes, one per lane: piece `piece` (rows keys), column group grp
+    const int groups = keys ? kColGroups : kAllGroups;
+    const int pieces = (keys ? kChunkBN : C::kVKeys) / rows;  // per slot
+    const int piece = lane / groups, grp = lane % groups;
+    const uint32_t dst0 = slot0 + grp * (pieces * box_bytes) + piece * box_bytes;
+    const bool has_box = lane < pieces * groups;
     int slot = 0, filled = 0;
     uint32_t phase = 0, q_count = 0;
+    uint32_t armed = 0, armed_phase = 0;  // this warp's slots and the phases that its last loads fill
     bool ok = true;
     const auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(bar, parity, abort_w));
       return ok;
     };
-    // lane l: the page of piece l (rows tokens) of a tile; negative: not loaded
-    const auto pages_of = [&](int tile) {
-      const uint32_t tok = static_cast<uint32_t>(tile) * kChunkBN + lane * rows;
-      int page = -2;
-      if (lane * rows < kChunkBN && tok < static_cast<uint32_t>(w.len) &&
-          tok + rows > static_cast<uint32_t>(w.lo_seq)) {
-        page = c.table[static_cast<int64_t>(w.b) * c.max_pages + tok / c.page_size];
-        if (page < 0 || page >= c.num_pages) {
-          report(FP8_DEV_BAD_INDEX);
-          page = -1;
-        }
-      }
-      return page;
-    };
-    // One slot: `groups` column groups from group g0 of the pieces from piece p0 on.
-    const auto load = [&](const CUtensorMap* map, int tile, int pages, int p0, int pieces, int g0, int groups) {
-      const int piece = p0 + lane / groups, grp = lane % groups;
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, piece & 31);
-      const bool mine = lane < pieces * groups && page >= 0;
-      const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes;
-      if (filled >= NS && !wait(empty0 + 8 * slot, phase ^ 1)) return;
-      if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot, bytes);
-      __syncwarp();
-      if (mine) {
-        const int in_page = static_cast<int>((static_cast<uint32_t>(tile) * kChunkBN + piece * rows) % c.page_size);
-        tma_load_page_cols(slot0 + slot * C::kSlotBytes + grp * (pieces * box_bytes) + (piece - p0) * box_bytes, map,
-                           full0 + 8 * slot, in_page, g0 + grp, w.h, page);
-      }
+    const auto pass = [&] {
       ++filled;
       if (++slot == NS) slot = 0, phase ^= 1;
     };
-    const auto load_k = [&](int tile, int pages) {
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p)
-        if (ok) load(&tmK, tile, pages, 0, kChunkBN / rows, p * kColGroups, kColGroups);
+    // lane l: page and place in it of piece l of a tile; page < 0: not loaded
+    const auto pages_of = [&](int tile) {
+      const uint32_t tok = static_cast<uint32_t>(tile) * kChunkBN + lane * rows;
+      int2 pg = make_int2(-2, 0);
+      if (lane * rows < kChunkBN && tok < static_cast<uint32_t>(w.len) &&
+          tok + rows > static_cast<uint32_t>(w.lo_seq)) {
+        const uint32_t i = tok / static_cast<uint32_t>(c.page_size);
+        pg.x = c.table[static_cast<int64_t>(w.b) * c.max_pages + i];
+        pg.y = tok - i * c.page_size;
+        if (pg.x < 0 || pg.x >= c.num_pages) {
+          report(FP8_DEV_BAD_INDEX);
+          pg.x = -1;
+        }
+      }
+      return pg;
     };
-    const auto load_v = [&](int tile, int pages) {
+    const auto load = [&](const int2& pg) {
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p)
-        if (ok) load(&tmV, tile, pages, p * (C::kVKeys / rows), C::kVKeys / rows, 0, kAllGroups);
+      for (int p = 0; p < PARTS; ++p) {
+        // key slots split the columns, value slots the keys
+        const int from = (keys ? 0 : p * pieces) + piece;
+        const int page = __shfl_sync(0xFFFFFFFFu, pg.x, from & 31);
+        const int token = __shfl_sync(0xFFFFFFFFu, pg.y, from & 31);
+        const bool mine = has_box && page >= 0;
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes;
+        if (filled >= NS && !wait(empty0 + 8 * slot, phase ^ 1)) return;
+        if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot, bytes);
+        __syncwarp();
+        if (mine)
+          tma_load_page_cols(dst0 + slot * C::kSlotBytes, map, full0 + 8 * slot, token,
+                             (keys ? p * kColGroups : 0) + grp, w.h, page);
+        armed |= 1u << slot;
+        armed_phase = (armed_phase & ~(1u << slot)) | (phase << slot);
+        pass();
+      }
+    };
+    const auto skip = [&] {
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) pass();
     };
     while (w.left > 0 && ok) {
       const int m = w.seg();
       const int tile = w.tile0 + w.t;
-      int pg = pages_of(tile);
-      load_k(tile, pg);
-      if (q_count > 0) wait(q_empty, (q_count - 1) & 1);
-      if (ok) ++q_count;
-      if (ok) {
-        const int nq = w.tile_tokens(1, tt1) > 0 && NT == 2 ? 2 : 1;
-        if (lane == 0) mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nq) * kAllGroups * tt1 * a.G * 128);
-        __syncwarp();
-        if (lane < nq * kAllGroups) {
-          const int i = lane / kAllGroups, grp = lane % kAllGroups;
-          tma_load_q(q_smem + i * (128 * D * 2) + grp * 16384, &tmQ, q_full, w.h * a.G,
-                     w.q0 + w.tok0 + i * tt1, grp);
+      int2 pg = pages_of(tile);
+      if (keys) {
+        load(pg);
+        if (q_count > 0) wait(q_empty, (q_count - 1) & 1);
+        if (ok) {
+          ++q_count;
+          const int nq = w.tile_tokens(1, tt1) > 0 && NT == 2 ? 2 : 1;
+          if (lane == 0)
+            mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(nq) * kAllGroups * tt1 * a.G * 128);
+          __syncwarp();
+          if (lane < nq * kAllGroups) {
+            const int i = lane / kAllGroups, qg = lane % kAllGroups;
+            tma_load_q(q_smem + i * (128 * D * 2) + qg * 16384, &tmQ, q_full, w.h * a.G,
+                       w.q0 + w.tok0 + i * tt1, qg);
+          }
         }
+        // order: K0 V0 K1 V1 ..., with two buffers for S K0 K1 V0 K2 V1 ...
+        int2 pg_next = m > 1 ? pages_of(tile + 1) : pg;
         for (int n = 0; n < m && ok; ++n) {
-          const int pg_next = n + 1 < m ? pages_of(tile + n + 1) : -2;
-          if (NT == 1 && n + 1 < m) load_k(tile + n + 1, pg_next);
-          load_v(tile + n, pg);
-          if (NT == 2 && n + 1 < m) load_k(tile + n + 1, pg_next);
+          pg = pg_next;
+          if (n + 2 < m) pg_next = pages_of(tile + n + 2);
+          if (NT == 2) skip();
+          if (n + 1 < m) load(pg);
+          if (NT == 1) skip();
+        }
+      } else {
+        skip();
+        for (int n = 0; n < m && ok; ++n) {
+          const int2 pg_next = n + 1 < m ? pages_of(tile + n + 1) : make_int2(-2, 0);
+          if (NT == 1 && n + 1 < m) skip();
+          load(pg);
+          if (NT == 2 && n + 1 < m) skip();
           pg = pg_next;
         }
       }
@@ -1264,9 +1452,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     }
     if (!ok && lane == 0) {
       // every copy started is waited for (bounded) before the CTA can exit
-      for (int i = max(0, filled - NS); i < filled; ++i) mbar_wait(full0 + 8 * (i % NS), (i / NS) & 1);
+      for (int i = 0; i < NS; ++i)
+        if (armed >> i & 1) mbar_wait(full0 + 8 * i, armed_phase >> i & 1);
       if (q_count > 0) mbar_wait(q_full, (q_count - 1) & 1);
     }
+  }
+  else {
+    if constexpr (NT == 2) regs_dec<72>();
   }
   tc_fence_before();
   __syncthreads();

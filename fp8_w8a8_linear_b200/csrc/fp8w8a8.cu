@@ -1428,6 +1428,10 @@ extern "C" fp8_status fp8_linear_bf16_noalloc(const uint16_t* x, const uint8_t* 
 // ============================================================ attention block
 namespace {
 
+// Largest number of new tokens, and of positions that a page table's row can
+// hold: the kernels' position arithmetic is in 32 bits.
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+
 // The cache and batch as the kernels see them, after the checks that the
 // append and the attention share.
 fp8_status paged_checked(const bf16_paged_kv* kv, int64_t T, PagedArgs* out) {
@@ -1437,7 +1441,9 @@ fp8_status paged_checked(const bf16_paged_kv* kv, int64_t T, PagedArgs* out) {
       kv->heads < 1 || kv->heads > 65536 || kv->head_dim < 1 || kv->page_stride < 0 ||
       kv->token_stride < 0 || kv->head_stride < 0)
     return FP8_ERR_INVALID_ARG;
-  if (kv->head_dim % 8 != 0 || kv->head_dim > 4096) return FP8_ERR_SHAPE;
+  if (kv->head_dim % 8 != 0 || kv->head_dim > 4096 || T > kMaxTokens ||
+      kv->max_pages * kv->page_size > kMaxTokens)
+    return FP8_ERR_SHAPE;
   // strides beyond 2^39 elements are beyond a tensor map (and any memory)
   const int64_t lim = int64_t(1) << 38;
   if (kv->page_stride > lim || kv->token_stride > lim || kv->head_stride > lim) return FP8_ERR_SHAPE;
@@ -1594,7 +1600,7 @@ fp8_status launch_attn_rows(const DeviceInfo& dev, AttnArgs a, const PagedArgs& 
                                       RowsCfg<D, S>::kSmem, stream, tmK, tmV, a, c))
     return st;
   const unsigned rows = static_cast<unsigned>(a.max_q * a.G);
-  return launch_pdl(attn_join_kernel<D, kRowsMax, 8>, dim3(ctas, rows), dim3(256), stream, a);
+  return launch_pdl(attn_join_rows_kernel<D>, dim3(ctas, rows), dim3(256), stream, a);
 }
 
 // Items of up to two (head_dim 256: one) tiles of 128 rows, one CTA per SM,
@@ -1620,7 +1626,7 @@ fp8_status launch_attn_chunk(const DeviceInfo& dev, AttnArgs a, const PagedArgs&
   if (fp8_status st = launch_pdl_smem(attn_chunk_kernel<D>, dim3(dev.sm_count), dim3(C::kThreads), C::kSmem,
                                       stream, tmQ, tmK, tmV, a, c))
     return st;
-  return launch_pdl(attn_join_kernel<D, C::kRows, 1>, dim3(dev.sm_count, C::kRows / 8), dim3(256), stream, a);
+  return launch_pdl(attn_join_chunk_kernel<D, C::kRows>, dim3(dev.sm_count, C::kRows / 32), dim3(256), stream, a);
 }
 
 }  // namespace
@@ -1660,7 +1666,7 @@ extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64
   a.Hq = static_cast<int>(q_heads);
   a.G = a.Hq / c.heads;
   a.max_q = static_cast<int>(max_q <= 0 ? T : std::min(max_q, T));
-  a.window = window > 0 && window < kMaxRows ? static_cast<int>(window) : static_cast<int>(kMaxRows);
+  a.window = static_cast<int>(window > 0 ? std::min(window, kMaxTokens) : kMaxTokens);
   a.scale_log2 = scale * 1.44269504088896341f;
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.part_o = reinterpret_cast<float*>(w);

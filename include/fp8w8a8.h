@@ -561,7 +561,7 @@ fp8_status fp8_linear_bf16_noalloc(const uint16_t* x, const uint8_t* w8, const f
  * expressed by them. Position j of sequence b is token j % page_size of page
  * page_table[b * max_pages + j / page_size]. Table entries behind a
  * sequence's last page are not read. The strides are multiples of 8 and the
- * arrays 16-byte aligned.
+ * arrays 16-byte aligned; max_pages * page_size and T are at most 2^30.
  */
 typedef struct bf16_paged_kv {
   uint16_t* k;

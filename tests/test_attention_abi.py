@@ -65,6 +65,7 @@ def test_kv_append_refusals(raw):
                 dict(token_stride=132), dict(head_stride=65)):
         assert go(kv=_kv(**bad)) == ALIGNMENT, bad
     assert go(kv=_kv(page_stride=1 << 40)) == SHAPE
+    assert go(kv=_kv(max_pages=(1 << 26) + 1)) == SHAPE and go(T=(1 << 30) + 1) == SHAPE
     assert go(ldk=132) == go(v=FAKE + 8) == ALIGNMENT
 
 
