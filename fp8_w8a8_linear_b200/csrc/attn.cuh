@@ -670,26 +670,31 @@ __global__ void __launch_bounds__(kRowsThreads)
 
 // ------------------------------------------------------------------ many rows
 // attn_chunk_kernel: items of up to NT x 128 rows on the tensor cores. Per
-// tile of 128 rows (128 / G tokens times the G heads of a group) and 128 keys:
+// tile of 128 rows (128 / G tokens times the G heads of a group) and unit of
+// keys:
 //   S = Q K^T        tcgen05, both operands in shared memory, S in TMEM;
-//   softmax          one thread per row: 128 scores from TMEM to registers,
-//                    P (bf16) back to TMEM over S;
+//   softmax          one thread per row: the unit's scores from TMEM to
+//                    registers, P (bf16) back to TMEM over S;
 //   O += P V         tcgen05, P from TMEM, V (keys x D) as a transposed
 //                    operand, O in TMEM.
-// Warps: four per row tile for the softmax, one that issues the MMAs, one that
-// loads. head_dim <= 128: two row tiles, so that one's softmax runs under the
-// other's MMAs. head_dim 256: o takes half of TMEM, so one row tile with two
-// buffers for S - the scores of the next keys are formed while the softmax
-// works on these. O is rescaled only when a row's maximum has grown by more
-// than 2^8 since the last time (the factor cancels in the end, and 2^8 times
-// a probability is as exact in bf16 and far from overflow in the sums): after
-// the first tiles hardly ever, so the softmax threads do it themselves.
-constexpr int kChunkBN = 128;
+// Warps: four per row tile for the softmax, one that issues the MMAs, two that
+// load (queries and keys; values). The softmax of 128 keys and the round trip
+// P -> O += P V -> next S are about as long (some 1700 and 1400 cycles), so
+// two are kept going: head_dim <= 128 with two row tiles in turn, head_dim 256
+// (whose O takes half of TMEM) with two buffers for S of its one row tile, the
+// next scores being formed under this softmax. P is handed over in two halves,
+// so that the product starts under the second half's exponentials.
+// O is rescaled only when a row's maximum has grown by more than 2^8 since
+// the last time (the factor cancels in the end, and 2^8 times a probability is
+// as exact in bf16 and far from overflow in the sums): after the first tiles
+// hardly ever, so the softmax threads do it themselves.
+constexpr int kChunkBN = 128;  // keys of a loaded tile
 
 template <int D>
 struct ChunkCfg {
-  static constexpr int kNT = D == 256 ? 1 : 2;    // row tiles of an item
-  static constexpr int kParts = D == 256 ? 2 : 1;  // slots per key tile and per value tile
+  static constexpr int kNT = D == 256 ? 1 : 2;       // row tiles of an item
+  static constexpr int kParts = D == 256 ? 2 : 1;    // slots per key tile and per value tile
+  static constexpr int kBufs = D == 256 ? 2 : 1;     // buffers for S per row tile
   static constexpr int kSlots = D == 64 ? 10 : 5;
   static constexpr int kSlotBytes = 128 * (D < 128 ? D : 128) * 2;
   static constexpr int kKCols = D < 128 ? D : 128;   // head elements of a key slot
@@ -697,8 +702,10 @@ struct ChunkCfg {
   static constexpr int kQBytes = kNT * 128 * D * 2;
   static constexpr int kThreads = kNT * 128 + 128;
   static constexpr int kRows = kNT * 128;            // rows of a part in the workspace
-  static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kSlots) * kSlotBytes +
-                                  8 * (2 * kSlots + 10) + 32 + sizeof(PlanSmem<kThreads>);
+  static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 2 + 2;  // see ChunkBars
+  static constexpr int kWalkInts = 16;
+  static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kSlots) * kSlotBytes + 8 * kBars + 16 +
+                                  sizeof(PlanSmem<kThreads>) + (kThreads / 32) * kWalkInts * 4;
 };
 
 // sum_{i < n} floor((a i + b) / m) for a n + b < 2^32 (the Euclid-like
@@ -730,22 +737,33 @@ __device__ __forceinline__ int block_tiles(int first, int window, int tok0, int 
   return max(1, (max(0, p0 + ntok) + kChunkBN - 1) / kChunkBN - tile0);
 }
 
-// The sum of block_tiles over a sequence's nb blocks of tt tokens.
+// sum_{i < n} floor((tt i + b) / 128), by shifts when tt is a power of two.
+__device__ __forceinline__ long long tile_sum(int n, int tt, int b) {
+  if (n <= 0) return 0;
+  if (tt & (tt - 1)) return floor_sum(n, kChunkBN, tt, b);
+  const long long nn = n;
+  if (tt >= kChunkBN) return nn * (nn - 1) / 2 * (tt / kChunkBN) + nn * (b / kChunkBN);
+  const int e = __ffs(tt) - 1, k = 7 - e;  // floor((i + c) / 2^k), c = floor(b / tt)
+  const auto below = [&](long long x) {    // sum_{i < x} floor(i / 2^k)
+    const long long q = x >> k;
+    return (q * (q - 1) / 2 << k) + q * (x - (q << k));
+  };
+  const long long cc = b >> e;
+  return below(nn + cc) - below(cc);
+}
+
+// The sum of block_tiles over a sequence's blocks of tt tokens.
 __device__ __forceinline__ long long chunk_tiles(int first, int len, int window, int tt, int ql) {
+  int tile0;
+  if (ql <= tt) return block_tiles(first, window, 0, ql, tile0);
   const int nb = (ql + tt - 1) / tt;
-  if (nb <= 8) {
-    long long s = 0;
-    int tile0;
-    for (int j = 0; j < nb; ++j) s += block_tiles(first, window, j * tt, min(tt, ql - j * tt), tile0);
-    return s;
-  }
   if (len == 0) return nb;
   const int je = first < 0 ? -first / tt : 0;  // blocks before position 0, one tile each
   long long s = je + (len + kChunkBN - 1) / kChunkBN +
-                floor_sum(nb - 1 - je, kChunkBN, tt, first + (je + 1) * tt + kChunkBN - 1);
+                tile_sum(nb - 1 - je, tt, first + (je + 1) * tt + kChunkBN - 1);
   const int x = first >= window ? -1 : window - 1 - first;
   const int jw = max(je, x < 0 ? 0 : x / tt + 1);  // first block that starts past tile 0's first key
-  if (nb > jw) s -= floor_sum(nb - jw, kChunkBN, tt, first + jw * tt - window + 1);
+  if (nb > jw) s -= tile_sum(nb - jw, tt, first + jw * tt - window + 1);
   return s;
 }
 
@@ -794,44 +812,51 @@ __device__ __forceinline__ void find_block(PlanSmem<THREADS>& sm, AttnRun& r, co
   r.tile = sm.run.tile;
 }
 
-// A run's segments: tiles t .. of item (sequence b, head h, block j).
+// A run's segments: tiles t .. of item (sequence b, head h, block j). Each
+// warp has one in shared memory (the fields are needed once a segment and
+// would cost the inner loops their registers); lane 0 moves it on.
 struct ChunkWalk {
   int b, h, j, t, left;
-  int q0, ql, len, first, nb;  // the sequence
-  int lo_seq;                  // keys below it no new token sees
-  int tt;
-  int tok0, ntok, tile0, n;    // the item: tokens tok0 .. of the sequence, key tiles tile0 .. + n
+  int q0, ql, len, first;  // the sequence
+  int lo_seq;              // keys below it no new token sees
+  int tok0, ntok, tile0, n;  // the item: tokens tok0 .. of the sequence, key tiles tile0 .. + n
+  uint32_t g;                // key tiles walked so far
 
   __device__ __forceinline__ bool seq(const AttnArgs& a, const PagedArgs& c) {
     const SeqSpan s = seq_span(a, c, b, kChunkBN);
     q0 = s.q0, ql = s.ql, len = s.len;
     first = len - ql;
     lo_seq = s.lo;
-    nb = (ql + tt - 1) / tt;
     return ql > 0;
   }
-  __device__ __forceinline__ void item(const AttnArgs& a) {
+  __device__ __forceinline__ void item(const AttnArgs& a, int tt) {
     tok0 = j * tt;
     ntok = min(ql - tok0, tt);
     n = block_tiles(first, a.window, tok0, ntok, tile0);
   }
-  __device__ __forceinline__ ChunkWalk(const AttnArgs& a, const PagedArgs& c, const AttnRun& r, int tt_) {
-    tt = tt_;
-    b = r.seq, left = r.units, h = r.head, j = r.block, t = r.tile;
-    if (left <= 0) return;
-    seq(a, c);
-    item(a);
+  __device__ __forceinline__ void start(const AttnArgs& a, const PagedArgs& c, const AttnRun& r, int tt) {
+    if (lane_id() == 0) {
+      b = r.seq, left = r.units, h = r.head, j = r.block, t = r.tile, g = 0;
+      if (left > 0) {
+        seq(a, c);
+        item(a, tt);
+      }
+    }
+    __syncwarp();
   }
   __device__ __forceinline__ int seg() const { return min(left, n - t); }
-  __device__ __forceinline__ void next(const AttnArgs& a, const PagedArgs& c, int m) {
+  // Past m tiles (one thread).
+  __device__ __forceinline__ void advance(const AttnArgs& a, const PagedArgs& c, int m, int tt) {
     left -= m;
+    g += m;
     t = 0;
     if (left <= 0) return;
-    if (++j == nb) {
+    ++j;
+    if (j * tt >= ql) {
       j = 0;
       if (++h == c.heads) {
         h = 0;
-        do {
+        do {  // left > 0: a sequence with new tokens follows
           if (++b >= c.batch) {
             left = 0;
             return;
@@ -839,10 +864,15 @@ struct ChunkWalk {
         } while (!seq(a, c));
       }
     }
-    item(a);
+    item(a, tt);
   }
-  // Row tile i (tt1 tokens each): its tokens, and the iterations [from, to)
-  // of the segment's m tiles in which it sees keys.
+  __device__ __forceinline__ void next(const AttnArgs& a, const PagedArgs& c, int m, int tt) {
+    __syncwarp();
+    if (lane_id() == 0) advance(a, c, m, tt);
+    __syncwarp();
+  }
+  // Row tile i (tt1 tokens each): its tokens, and those of the segment's m key
+  // tiles, [from, to), in which it sees keys.
   __device__ __forceinline__ int tile_tokens(int i, int tt1) const { return max(0, min(tt1, ntok - i * tt1)); }
   __device__ __forceinline__ void tile_range(const AttnArgs& a, int i, int tt1, int m, int& from, int& to) const {
     const int nt = tile_tokens(i, tt1);
@@ -852,12 +882,11 @@ struct ChunkWalk {
     const int lo = (p0 < a.window ? 0 : p0 - a.window + 1) / kChunkBN;
     const int hi = max(lo + 1, (max(0, p0 + nt) + kChunkBN - 1) / kChunkBN);
     from = max(0, lo - tile0 - t);
-    to = min(m, hi - tile0 - t);
-    if (to < from) to = from;
+    to = max(from, min(m, hi - tile0 - t));
   }
 };
 
-// ---- tcgen05 with A in TMEM, TMEM stores, transposed-B descriptor
+// tcgen05.mma with A in TMEM, issued by one thread.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -916,16 +945,6 @@ __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map,
       : "memory");
 }
 
-// A warpgroup's share of the block's registers (whole warpgroups call it).
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // The largest of three (one instruction).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -968,7 +987,27 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&u)[4][4], int lane) {
   }
 }
 
-// The softmax of one row tile's rows, one thread per row.
+// The probabilities of 64 keys from their scores (pairs of bf16, to TMEM),
+// added up in sum.
+__device__ __forceinline__ void chunk_probs(const uint32_t (&s)[64], float scale, float shift, uint32_t p_addr, float2 (&sum)[2]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float x0, x1;
+      ffma2(x0, x1, __uint_as_float(s[32 * q + e]), __uint_as_float(s[32 * q + e + 1]), scale, shift);
+      x0 = ex2(x0);
+      x1 = ex2(x1);
+      fadd2(sum[(e / 2) & 1], x0, x1);
+      pk[e / 2] = pack_bf16x2(x0, x1);
+    }
+    tmem_st16(p_addr + 16 * q, pk);
+  }
+}
+
+// The softmax of one row tile's rows, one thread per row. s_full, p_full: the
+// tile's barriers, one and two (halves) per buffer.
 template <int D>
 __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs& c, ChunkWalk& w, int tile,
                                               int tt1, uint32_t tmem, uint32_t s_full, uint32_t p_full,
@@ -977,10 +1016,9 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
   const int lane = lane_id(), quad = warp_id() & 3;
   const int rr = 32 * quad + lane;  // row of the tile
   const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-  const uint32_t o_addr = tmem + lanes + 256 + tile * D;
+  const uint32_t s_addr0 = tmem + lanes + tile * C::kBufs * kChunkBN, o_addr = tmem + lanes + 256 + tile * D;
   const int cta = blockIdx.x;
-  uint32_t count[2] = {0, 0};  // uses of the S buffers
-  uint32_t done = 0;           // products with V so far
+  uint32_t done = 0;  // key tiles so far: products with V asked for
   bool ok = true;
   int4 desc = make_int4(0, 0, 0, 0);
   for (bool first_seg = true; w.left > 0 && ok; first_seg = false) {
@@ -989,45 +1027,43 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
     w.tile_range(a, tile, tt1, m, from, to);
     const int ntok = w.tile_tokens(tile, tt1);
     const int p0 = w.first + w.tok0 + tile * tt1;  // positions p0 .. p0 + ntok - 1
-    const int pos = p0 + rr / a.G;
+    const int key_seg = (w.tile0 + w.t) * kChunkBN;
+    const int rel0 = p0 + rr / a.G - key_seg;      // this row's position, from the segment's first key
     float mu = -INFINITY, l = 0.0f;
-    for (int i = from; i < to; ++i) {
-      const int buf = C::kNT == 2 ? tile : i & 1;
-      const uint32_t s_addr = tmem + lanes + 128 * buf;
-      const int key0 = (w.tile0 + w.t + i) * kChunkBN;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(s_full + 8 * buf, count[buf] & 1, abort_w));
+    for (int u = from; u < to && ok; ++u) {
+      const uint32_t buf = C::kBufs == 2 ? done & 1 : 0;
+      const uint32_t s_addr = s_addr0 + buf * kChunkBN;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(s_full + 8 * buf, (C::kBufs == 2 ? done >> 1 : done) & 1, abort_w));
       if (!ok) break;
-      ++count[buf];
       tc_fence_after();
-      uint32_t s[4][32];
+      const int key0 = key_seg + kChunkBN * u;
+      const bool edge = key0 + kChunkBN - 1 > p0 || p0 + ntok - 1 - key0 >= a.window;
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t x[64];
+        tmem_ld32(s_addr + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(x));
+        tmem_ld32(s_addr + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+        tmem_ld_wait();
+        if (edge) {
+          const int rel = rel0 - kChunkBN * u - 64 * half;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s[q]);
-      tmem_ld_wait();
-      if (key0 + kChunkBN - 1 > p0 || p0 + ntok - 1 - key0 >= a.window) {  // some row's edge
-        const int rel = pos - key0;
+          for (int e = 0; e < 64; ++e)
+            if (static_cast<uint32_t>(rel - e) >= static_cast<uint32_t>(a.window)) x[e] = 0xFF800000u;
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (static_cast<uint32_t>(rel - (32 * q + e)) >= static_cast<uint32_t>(a.window))
-              s[q][e] = 0xFF800000u;
+          for (int e = 0; e < 16; e += 2) mx[q] = max3(mx[q], __uint_as_float(x[16 * q + e]), __uint_as_float(x[16 * q + e + 1]));
       }
-      float mx[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        mx[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
-#pragma unroll
-        for (int e = 2; e < 32; e += 2)
-          mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
       const bool grow = top > mu + 8.0f;
       if (__any_sync(0xFFFFFFFFu, grow)) {
         const float nm = grow ? top : mu;
         const float f = grow ? ex2(mu - nm) : 1.0f;  // mu = -inf: 0 (l and o are 0)
         l *= f;
         mu = nm;
-        if (i > from) {  // o holds the earlier keys: wait for their product
+        if (u > from) {  // o holds the earlier keys: wait for their product
           ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(o_done, (done - 1) & 1, abort_w));
           if (!ok) break;
           tc_fence_after();
@@ -1044,25 +1080,27 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
       }
       const float shift = mu == -INFINITY ? 0.0f : -mu;
       float2 sum[2] = {};
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t x[64];
+        tmem_ld32(s_addr + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(x));
+        tmem_ld32(s_addr + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+        tmem_ld_wait();
+        if (edge) {
+          const int rel = rel0 - kChunkBN * u - 64 * half;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float x0, x1;
-          ffma2(x0, x1, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]), a.scale_log2, shift);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          fadd2(sum[q & 1], x0, x1);
-          pk[e / 2] = pack_bf16x2(x0, x1);
+          for (int e = 0; e < 64; ++e)
+            if (static_cast<uint32_t>(rel - e) >= static_cast<uint32_t>(a.window)) x[e] = 0xFF800000u;
         }
-        tmem_st16(s_addr + 16 * q, pk);
+        chunk_probs(x, a.scale_log2, shift, s_addr + 32 * half, sum);
+        if (C::kBufs == 2 && half == 0 && u + 1 == to && u > from)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(o_done, (done - 1) & 1, abort_w));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 16 * buf + 8 * half);
       }
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + 8 * buf);
       ++done;
     }
     if (!ok) break;
@@ -1074,10 +1112,7 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
     const int64_t tok = w.q0 + w.tok0 + tile * tt1 + rr / a.G;
     const int head = w.h * a.G + rr % a.G;
     if (to > from) {
-      // The last product, by way of the one before it: with two buffers for S
-      // neither need be done yet, and a parity tells only adjacent phases apart.
-      if (C::kNT == 1 && to - from > 1) ok = mbar_wait_ab(o_done, done & 1, abort_w);
-      ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_ab(o_done, (done - 1) & 1, abort_w));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(o_done, (done - 1) & 1, abort_w));
       if (!ok) break;
       tc_fence_after();
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -1128,9 +1163,150 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
     }
     if (w.t == 0 && !whole)
       desc = join_desc((w.n - m + per - 1) / per, part, w.q0 + w.tok0, w.h * a.G, w.ntok * a.G);
-    w.next(a, c, m);
+    w.next(a, c, m, C::kNT * tt1);
   }
   if (tile == 0 && rr == 0) a.part_desc[cta] = ok ? desc : make_int4(0, 0, 0, 0);
+}
+
+// Barriers of the chunk kernel, by their addresses' offsets: full[kSlots],
+// empty[kSlots], queries full and empty, S full (per buffer), P full (two
+// halves per buffer), O done (per row tile), the V loader's own, drained.
+template <int D>
+struct ChunkBars {
+  using C = ChunkCfg<D>;
+  static constexpr uint32_t kEmpty = 8 * C::kSlots, kQFull = 16 * C::kSlots, kQEmpty = kQFull + 8, kSFull = kQFull + 16,
+                            kPFull = kSFull + 16, kODone = kPFull + 32, kVTmp = kODone + 16, kDrained = kVTmp + 8;
+  static_assert(kDrained + 8 == 8 * C::kBars, "barriers");
+};
+
+// The MMAs, issued by one thread. It shares its scheduler and instruction
+// cache with two softmax warps, so what it does between two products counts:
+// the slots' waits come before the probabilities' and the releases last.
+template <int D>
+__device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedArgs& c, ChunkWalk& w, int tt1,
+                                                uint32_t tmem, uint32_t q_smem, uint32_t slot0, uint32_t bars,
+                                                uint32_t abort_w, bool& issued) {
+  using C = ChunkCfg<D>;
+  using B = ChunkBars<D>;
+  constexpr int NT = C::kNT, NS = C::kSlots, PARTS = C::kParts;
+  constexpr uint32_t kIdescS = idesc_kind<kKindBF16>(128, kChunkBN);
+  constexpr uint32_t kIdescO = idesc_kind<kKindBF16>(128, D) | kIdescBMnMajor;
+  const uint32_t q_lo = desc_lo(q_smem, 16), k_lo = desc_lo(slot0, 16), v_lo = desc_lo(slot0, C::kVKeys * 128);
+  int slot = 0;  // next slot in load order
+  uint32_t phase = 0, q_par = 0, p_par = 0;
+  const auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_ab(bars + bar, parity, abort_w); };
+  // Waits for the next PARTS slots; they are used in load order.
+  const auto take = [&](int (&at)[PARTS]) {
+    bool ok = true;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      at[p] = slot;
+      ok = ok && wait(8 * slot, phase);
+      if (++slot == NS) slot = 0, phase ^= 1;
+    }
+    return ok;
+  };
+  const auto release = [&](const int (&at)[PARTS]) {
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) umma_commit(bars + B::kEmpty + 8 * at[p]);
+  };
+  // S of a key tile for row tile `tile` into its buffer `buf`.
+  const auto scores = [&](int tile, uint32_t buf, const int (&at)[PARTS]) {
+    const uint32_t b = tile * C::kBufs + buf;
+    uint32_t kb[PARTS];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) kb[p] = k_lo + at[p] * (C::kSlotBytes / 16);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const int p = k * 16 / C::kKCols, kk = k - p * (C::kKCols / 16);
+      umma_kind<kKindBF16>(tmem + b * kChunkBN,
+                           desc_of(q_lo + (tile * (128 * D * 2) + (k >> 2) * 16384 + (k & 3) * 32) / 16),
+                           desc_of(kb[p] + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16), kIdescS, k > 0);
+    }
+    umma_commit(bars + B::kSFull + 8 * b);
+    issued = true;
+  };
+  // Adds the product of P, as its halves come, with V.
+  const auto product = [&](int tile, uint32_t buf, const int (&at)[PARTS], bool add) {
+    const uint32_t b = tile * C::kBufs + buf, par = p_par >> b & 1;
+    p_par ^= 1u << b;
+    uint32_t vb[PARTS];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) vb[p] = v_lo + at[p] * (C::kSlotBytes / 16);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (!wait(B::kPFull + 16 * b + 8 * half, par)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 4 * half; k < 4 * half + 4; ++k) {
+        const int p = k * 16 / C::kVKeys, kk = k - p * (C::kVKeys / 16);
+        umma_bf16_ts(tmem + 256 + tile * D, tmem + b * kChunkBN + 8 * k, desc_of(vb[p] + kk * 128), kIdescO,
+                     k > 0 ? 1u : static_cast<uint32_t>(add));
+      }
+    }
+    umma_commit(bars + B::kODone + 8 * tile);
+    return true;
+  };
+  while (w.left > 0) {
+    const int m = w.seg();
+    int from[NT], to[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) w.tile_range(a, i, tt1, m, from[i], to[i]);
+    int kat[PARTS], vat[PARTS];
+    if (!wait(B::kQFull, q_par)) return false;
+    q_par ^= 1;
+    if (!take(kat)) return false;
+    tc_fence_after();
+    if constexpr (NT == 2) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (from[i] == 0 && to[i] > 0) scores(i, 0, kat);
+      release(kat);
+      if (m == 1) umma_commit(bars + B::kQEmpty);
+      for (int n = 0; n < m; ++n) {
+        const bool next = n + 1 < m;
+        if (!take(vat) || (next && !take(kat))) return false;
+        // per row tile: O += P V of this key tile, then S of the next over P
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (n >= from[i] && n < to[i] && !product(i, 0, vat, n > from[i])) return false;
+          if (next && n + 1 >= from[i] && n + 1 < to[i]) scores(i, 0, kat);
+        }
+        release(vat);
+        if (next) release(kat);
+        if (n + 2 == m) umma_commit(bars + B::kQEmpty);
+      }
+    } else {
+      scores(0, w.g & 1, kat);
+      release(kat);
+      if (m == 1) umma_commit(bars + B::kQEmpty);
+      for (int n = 0; n < m; ++n) {
+        const uint32_t buf = (w.g + n) & 1;
+        if (n + 1 < m) {
+          if (!take(kat)) return false;
+          tc_fence_after();
+          scores(0, buf ^ 1, kat);
+          release(kat);
+          if (n + 2 == m) umma_commit(bars + B::kQEmpty);
+        }
+        if (!take(vat) || !product(0, buf, vat, n > 0)) return false;
+        release(vat);
+      }
+    }
+    w.advance(a, c, m, NT * tt1);
+  }
+  return true;
+}
+
+template <int D>
+__device__ __forceinline__ void chunk_issue(const AttnArgs& a, const PagedArgs& c, ChunkWalk& w, int tt1, uint32_t tmem,
+                                            uint32_t q_smem, uint32_t slot0, uint32_t bars, uint32_t abort_w) {
+  bool issued = false;
+  if (!chunk_issue_all<D>(a, c, w, tt1, tmem, q_smem, slot0, bars, abort_w, issued) && issued) {
+    // everything issued is done before TMEM is given back (bounded)
+    umma_commit(bars + ChunkBars<D>::kDrained);
+    mbar_wait(bars + ChunkBars<D>::kDrained, 0);
+  }
 }
 
 template <int D>
@@ -1143,13 +1319,16 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   uint8_t* smem = align1024(smem_raw);
   uint8_t* slots = smem + C::kQBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(slots + NS * C::kSlotBytes);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * NS;
-  const uint32_t q_full = empty0 + 8 * NS, q_empty = q_full + 8;
-  const uint32_t s_full = q_empty + 8, p_full = s_full + 16, o_done = p_full + 16, drained = o_done + 16;
-  uint32_t* words = reinterpret_cast<uint32_t*>(bars + 2 * NS + 10);
+  using B = ChunkBars<D>;
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + B::kEmpty, q_full = full0 + B::kQFull,
+                 q_empty = full0 + B::kQEmpty, s_full = full0 + B::kSFull, p_full = full0 + B::kPFull,
+                 o_done = full0 + B::kODone, v_tmp = full0 + B::kVTmp;
+  auto* plan = reinterpret_cast<PlanSmem<C::kThreads>*>(bars + C::kBars);
+  uint32_t* words = reinterpret_cast<uint32_t*>(plan + 1);
   const uint32_t abort_w = smem_u32(words);
   uint32_t* tmem_holder = words + 1;
-  auto* plan = reinterpret_cast<PlanSmem<C::kThreads>*>(words + 8);
+  static_assert(sizeof(ChunkWalk) <= C::kWalkInts * 4, "walks");
+  auto& w = *reinterpret_cast<ChunkWalk*>(words + 4 + C::kWalkInts * warp_id());
   const uint32_t q_smem = smem_u32(smem), slot0 = smem_u32(slots);
   const int warp = warp_id(), lane = lane_id();
   constexpr int kMmaWarp = NT * 4, kLoadWarp = NT * 4 + 1;  // and kLoadWarp + 1
@@ -1162,12 +1341,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(drained, 1);
+    mbar_init(v_tmp, 1);
+    mbar_init(full0 + B::kDrained, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 4);
       mbar_init(o_done + 8 * i, 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(p_full + 8 * i, 4);
     fence_barrier_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
@@ -1191,159 +1371,16 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     return chunk_tiles(s.len - s.ql, s.len, a.window, tt, s.ql) * c.heads;
   });
   find_block(*plan, run, a, c, tt);
-  ChunkWalk w(a, c, run, tt);
+  w.start(a, c, run, tt);
 
-  // Two row tiles: 384 threads of 168 registers at launch; the softmax keeps
-  // a row's 128 scores in registers, so its warps take 216 and the issuing
-  // ones 72 (2 x 128 x 216 + 128 x 72 = 384 x 168). One row tile: 256
-  // threads have 255 each as it is.
   if (warp < kMmaWarp) {
-    if constexpr (NT == 2) regs_inc<216>();
     const int tile = warp >> 2;
-    chunk_softmax<D>(a, c, w, tile, tt1, tmem, s_full, p_full, o_done + 8 * tile, abort_w, run.per);
+    chunk_softmax<D>(a, c, w, tile, tt1, tmem, s_full + 8 * tile, p_full + 16 * tile, o_done + 8 * tile, abort_w,
+                     run.per);
   } else if (warp == kMmaWarp) {
-    if constexpr (NT == 2) regs_dec<72>();
-    // ------------------------------------------------------------- MMA issue
-    constexpr uint32_t kIdescS = idesc_kind<kKindBF16>(128, kChunkBN);
-    constexpr uint32_t kIdescO = idesc_kind<kKindBF16>(128, D) | kIdescBMnMajor;
-    const uint32_t q_lo = desc_lo(q_smem, 16), k_lo = desc_lo(slot0, 16), v_lo = desc_lo(slot0, C::kVKeys * 128);
-    int slot = 0;            // next slot in load order
-    uint32_t phase = 0;
-    uint32_t q_count = 0, p_count[2] = {0, 0};
-    bool ok = true, issued = false;
-    const auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(bar, parity, abort_w));
-      return ok;
-    };
-    // Waits for the next PARTS slots and returns the first; they are used in
-    // load order.
-    const auto take = [&](int (&at)[PARTS]) {
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p) {
-        at[p] = slot;
-        wait(full0 + 8 * slot, phase);
-        if (++slot == NS) slot = 0, phase ^= 1;
-      }
-    };
-    const auto release = [&](const int (&at)[PARTS]) {
-      if (ok && lane == 0)
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) umma_commit(empty0 + 8 * at[p]);
-    };
-    const auto release_q = [&] {  // after the segment's last scores
-      if (ok && lane == 0) umma_commit(q_empty);
-    };
-    const auto scores = [&](int tile, int buf, const int (&at)[PARTS]) {
-      if (ok && lane == 0) {
-        tc_fence_after();
-        uint32_t kb[PARTS];
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) kb[p] = k_lo + at[p] * (C::kSlotBytes / 16);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const int p = k * 16 / C::kKCols, kk = k - p * (C::kKCols / 16);
-          umma_kind<kKindBF16>(tmem + 128 * buf,
-                               desc_of(q_lo + (tile * (128 * D * 2) + (k >> 2) * 16384 + (k & 3) * 32) / 16),
-                               desc_of(kb[p] + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16), kIdescS, k > 0);
-        }
-        umma_commit(s_full + 8 * buf);
-      }
-      issued = true;
-    };
-    const auto product = [&](int tile, int buf, const int (&at)[PARTS], bool add) {
-      if (ok && lane == 0) {
-        tc_fence_after();
-        uint32_t vb[PARTS];
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) vb[p] = v_lo + at[p] * (C::kSlotBytes / 16);
-#pragma unroll
-        for (int k = 0; k < kChunkBN / 16; ++k) {
-          const int p = k * 16 / C::kVKeys, kk = k - p * (C::kVKeys / 16);
-          umma_bf16_ts(tmem + 256 + tile * D, tmem + 128 * buf + 8 * k, desc_of(vb[p] + kk * 2048 / 16), kIdescO,
-                       k > 0 ? 1u : static_cast<uint32_t>(add));
-        }
-        umma_commit(o_done + 8 * tile);
-      }
-    };
-    // Value rows that are not keys of the sequence's new tokens hold anything
-    // (or were not loaded): zeros, which the zero probabilities leave alone.
-    const auto clear = [&](const int (&at)[PARTS], int key0) {
-      const int lo = w.lo_seq - key0, hi = w.len - key0;  // rows [lo, hi) count
-      if (lo <= 0 && hi >= kChunkBN) return;
-#pragma unroll
-      for (int p = 0; p < PARTS; ++p)
-        for (int r = 0; r < C::kVKeys; ++r) {
-          const int key = p * C::kVKeys + r;
-          if (key >= lo && key < hi) continue;
-          if (lane < D / 8)
-            *reinterpret_cast<uint4*>(slots + at[p] * C::kSlotBytes + (lane >> 3) * (C::kVKeys * 128) + r * 128 +
-                                      (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-      fence_proxy_async_shared();
-      __syncwarp();
-    };
-    while (w.left > 0 && ok) {
-      const int m = w.seg();
-      int from[NT], to[NT];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) w.tile_range(a, i, tt1, m, from[i], to[i]);
-      const int tile_first = w.tile0 + w.t;
-      wait(q_full, q_count & 1);
-      ++q_count;
-      int kat[PARTS], vat[PARTS];
-      take(kat);
-      if constexpr (NT == 2) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (from[i] == 0 && to[i] > 0) scores(i, i, kat);
-        release(kat);
-        if (m == 1) release_q();
-        for (int n = 0; n < m && ok; ++n) {
-          take(vat);
-          clear(vat, (tile_first + n) * kChunkBN);
-          bool next = n + 1 < m;
-          if (next) take(kat);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (n >= from[i] && n < to[i]) {
-              wait(p_full + 8 * i, p_count[i] & 1);
-              ++p_count[i];
-              product(i, i, vat, n > from[i]);
-            }
-            if (next && n + 1 >= from[i] && n + 1 < to[i]) scores(i, i, kat);
-          }
-          if (next) release(kat);
-          if (n + 2 == m) release_q();
-          release(vat);
-        }
-      } else {
-        scores(0, 0, kat);
-        release(kat);
-        if (m == 1) release_q();
-        for (int n = 0; n < m && ok; ++n) {
-          if (n + 1 < m) {
-            take(kat);
-            scores(0, (n + 1) & 1, kat);
-            release(kat);
-            if (n + 2 == m) release_q();
-          }
-          take(vat);
-          clear(vat, (tile_first + n) * kChunkBN);
-          wait(p_full + 8 * (n & 1), p_count[n & 1] & 1);
-          ++p_count[n & 1];
-          product(0, n & 1, vat, n > 0);
-          release(vat);
-        }
-      }
-      w.next(a, c, m);
-    }
-    if (!ok && issued && lane == 0) {
-      // everything issued is done before TMEM is given back (bounded)
-      umma_commit(drained);
-      mbar_wait(drained, 0);
-    }
+    if (lane == 0) chunk_issue<D>(a, c, w, tt1, tmem, q_smem, slot0, full0, abort_w);
   } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
-    if constexpr (NT == 2) regs_dec<72>();
+    
     // ------------------------------------------------------------- loads
     // One warp for queries and keys, one for values; they share the ring,
     // whose order both know, and each passes over the other's slots.
@@ -1386,7 +1423,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       }
       return pg;
     };
-    const auto load = [&](const int2& pg) {
+    uint32_t v_par = 0;
+    bool v_tmp_armed = false;
+    const auto load = [&](const int2& pg, int key0) {
+      // Value rows that are not keys of the sequence's new tokens hold anything
+      // (or are not loaded): zeros, which the zero probabilities leave alone.
+      // Such a tile comes in on a barrier of the loader's own, is cleared, and
+      // then handed on.
+      const int lo = w.lo_seq - key0, hi = w.len - key0;  // rows [lo, hi) count
+      const bool edge = !keys && (lo > 0 || hi < kChunkBN);
 #pragma unroll
       for (int p = 0; p < PARTS; ++p) {
         // key slots split the columns, value slots the keys
@@ -1396,13 +1441,30 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         const bool mine = has_box && page >= 0;
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes;
         if (filled >= NS && !wait(empty0 + 8 * slot, phase ^ 1)) return;
-        if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot, bytes);
+        const uint32_t bar = edge ? v_tmp : full0 + 8 * slot;
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         __syncwarp();
         if (mine)
-          tma_load_page_cols(dst0 + slot * C::kSlotBytes, map, full0 + 8 * slot, token,
-                             (keys ? p * kColGroups : 0) + grp, w.h, page);
-        armed |= 1u << slot;
-        armed_phase = (armed_phase & ~(1u << slot)) | (phase << slot);
+          tma_load_page_cols(dst0 + slot * C::kSlotBytes, map, bar, token, (keys ? p * kColGroups : 0) + grp, w.h,
+                             page);
+        if (edge) {
+          v_tmp_armed = true;
+          if (!wait(v_tmp, v_par)) return;
+          v_tmp_armed = false;
+          v_par ^= 1;
+          for (int r = 0; r < C::kVKeys; ++r) {
+            const int key = p * C::kVKeys + r;
+            if ((key < lo || key >= hi) && lane < D / 8)
+              *reinterpret_cast<uint4*>(slots + slot * C::kSlotBytes + (lane >> 3) * (C::kVKeys * 128) + r * 128 +
+                                        (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full0 + 8 * slot);
+        } else {
+          armed |= 1u << slot;
+          armed_phase = (armed_phase & ~(1u << slot)) | (phase << slot);
+        }
         pass();
       }
     };
@@ -1415,7 +1477,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       const int tile = w.tile0 + w.t;
       int2 pg = pages_of(tile);
       if (keys) {
-        load(pg);
+        if (q_count > 0) load(pg, 0);  // under the last segment's end; the first queries come first
         if (q_count > 0) wait(q_empty, (q_count - 1) & 1);
         if (ok) {
           ++q_count;
@@ -1428,6 +1490,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
             tma_load_q(q_smem + i * (128 * D * 2) + qg * 16384, &tmQ, q_full, w.h * a.G,
                        w.q0 + w.tok0 + i * tt1, qg);
           }
+          if (q_count == 1) load(pg, 0);
         }
         // order: K0 V0 K1 V1 ..., with two buffers for S K0 K1 V0 K2 V1 ...
         int2 pg_next = m > 1 ? pages_of(tile + 1) : pg;
@@ -1435,7 +1498,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           pg = pg_next;
           if (n + 2 < m) pg_next = pages_of(tile + n + 2);
           if (NT == 2) skip();
-          if (n + 1 < m) load(pg);
+          if (n + 1 < m) load(pg, 0);
           if (NT == 1) skip();
         }
       } else {
@@ -1443,22 +1506,20 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         for (int n = 0; n < m && ok; ++n) {
           const int2 pg_next = n + 1 < m ? pages_of(tile + n + 1) : make_int2(-2, 0);
           if (NT == 1 && n + 1 < m) skip();
-          load(pg);
+          load(pg, (tile + n) * kChunkBN);
           if (NT == 2 && n + 1 < m) skip();
           pg = pg_next;
         }
       }
-      w.next(a, c, m);
+      w.next(a, c, m, tt);
     }
     if (!ok && lane == 0) {
       // every copy started is waited for (bounded) before the CTA can exit
       for (int i = 0; i < NS; ++i)
         if (armed >> i & 1) mbar_wait(full0 + 8 * i, armed_phase >> i & 1);
       if (q_count > 0) mbar_wait(q_full, (q_count - 1) & 1);
+      if (v_tmp_armed) mbar_wait(v_tmp, v_par);
     }
-  }
-  else {
-    if constexpr (NT == 2) regs_dec<72>();
   }
   tc_fence_before();
   __syncthreads();
