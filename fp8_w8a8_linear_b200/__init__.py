@@ -549,7 +549,7 @@ def _current(t: torch.Tensor, name: str):
     """The current device and its current stream, once per call; t is the call's first tensor."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
@@ -561,11 +561,11 @@ def _ptr(t: torch.Tensor, dtype, dev: int, name: str) -> int:
     return t.data_ptr()
 
 
-def _pitch(t: torch.Tensor, name: str) -> int:
-    """Token pitch of a [T, heads, head_dim] tensor whose heads lie side by side."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have shape [T, heads, head_dim], got {tuple(t.shape)}")
-    T, H, D = t.shape
+def _pitch(t: torch.Tensor, shape, name: str) -> int:
+    """Token pitch of a tensor of shape [T, heads, head_dim] whose heads lie side by side."""
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have shape [T, heads, head_dim], got {tuple(shape)}")
+    T, H, D = shape
     if t.is_contiguous():
         return H * D
     st = t.stride()
@@ -574,31 +574,43 @@ def _pitch(t: torch.Tensor, name: str) -> int:
     return st[0] if T > 1 else H * D
 
 
-def _vec(t: torch.Tensor, dtype, n: int, dev: int, name: str) -> int:
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape ({n},), got {tuple(t.shape)}")
-    return _ptr(t, dtype, dev, name)
-
-
-def _same(t: torch.Tensor, shape, name: str):
+def _like_pitch(t: torch.Tensor, shape, name: str) -> int:
+    """The same for a tensor that must have `shape`."""
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _pitch(t, shape, name)
 
 
-def _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, head_dim: int, dev: int):
-    if k_cache.dim() != 4 or k_cache.shape[3] != head_dim:
-        raise ValueError(f"k_cache must be [pages, page_size, heads, {head_dim}], got {tuple(k_cache.shape)}")
-    pages, page_size, heads, _ = shape = k_cache.shape
-    st = k_cache.stride()
+def _vec(t: torch.Tensor, dtype, n: int, dev: int, name: str) -> int:
+    if t.numel() != n or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape ({n},), got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A new contiguous tensor of t's shape and type (empty_like is the quicker call where t is contiguous)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
+def _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, heads: int | None, head_dim: int, dev: int):
+    shape, st = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or shape[3] != head_dim or (heads is not None and shape[2] != heads):
+        raise ValueError(f"k_cache must be [pages, page_size, {'heads' if heads is None else heads}, {head_dim}], "
+                         f"got {tuple(shape)}")
     if v_cache.shape != shape or v_cache.stride() != st:
         raise ValueError("v_cache must have the shape and strides of k_cache")
     if st[3] != 1:
         raise ValueError("k_cache: the elements of a head must lie side by side")
-    if page_table.dim() != 2 or not page_table.is_contiguous():
+    table = page_table.shape
+    if len(table) != 2 or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous [batch, max_pages] tensor")
-    batch, max_pages = page_table.shape
-    return _PAGED_KV.pack(_ptr(k_cache, _BF16, dev, "k_cache"), _ptr(v_cache, _BF16, dev, "v_cache"), pages, page_size,
-                          heads, head_dim, st[0], st[1], st[2], _ptr(page_table, _I32, dev, "page_table"), batch,
+    batch, max_pages = table
+    return _PAGED_KV.pack(_ptr(k_cache, _BF16, dev, "k_cache"), _ptr(v_cache, _BF16, dev, "v_cache"), shape[0], shape[1],
+                          shape[2], head_dim, st[0], st[1], st[2], _ptr(page_table, _I32, dev, "page_table"), batch,
                           max_pages, _vec(cu_q, _I32, batch + 1, dev, "cu_q"),
                           _vec(kv_lens, _I32, batch, dev, "kv_lens"))
 
@@ -644,13 +656,13 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, inter
     """x bf16 [T, heads, head_dim] with the first 2 * len(inv_freq) elements of each head turned by positions int32 [T]
     (y may be x)."""
     dev, stream = _current(x, "x")
-    ldx = _pitch(x, "x")
-    T, H, D = shape = x.shape
+    shape = x.shape
+    ldx = _pitch(x, shape, "x")
+    T, H, D = shape
     if y is None:
-        y, ldy = x.new_empty(shape), H * D
+        y, ldy = _like(x), H * D
     else:
-        _same(y, shape, "y")
-        ldy = _pitch(y, "y")
+        ldy = _like_pitch(y, shape, "y")
     R = inv_freq.numel()
     _check(_lib.bf16_rope(_ptr(x, _BF16, dev, "x"), ldx, _vec(positions, _I32, T, dev, "positions"),
                           _vec(inv_freq, _F32, R, dev, "inv_freq"), T, H, D, 2 * R, interleaved, amplitude,
@@ -667,24 +679,23 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     [T, q_heads, head_dim] the queries are turned too, into q_out (new when None; may be q), which is returned.
     page_table int32 [batch, max_pages], cu_q int32 [batch + 1], kv_lens int32 [batch] (the new tokens counted)."""
     dev, stream = _current(k, "k")
-    ldk, ldv = _pitch(k, "k"), _pitch(v, "v")
-    T, H, D = shape = k.shape
-    _same(v, shape, "v")
-    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, D, dev)
-    if k_cache.shape[2] != H:
-        raise ValueError(f"k has {H} heads, the cache {k_cache.shape[2]}")
+    shape = k.shape
+    ldk, ldv = _pitch(k, shape, "k"), _like_pitch(v, shape, "v")
+    T, H, D = shape
+    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, H, D, dev)
     qp = qop = fp = None
     ldq = ldqo = Hq = R = 0
     if q is not None:
-        ldq = _pitch(q, "q")
-        Hq = q.shape[1]
-        _same(q, (T, Hq, D), "q")
+        qs = q.shape
+        ldq = _pitch(q, qs, "q")
+        Hq = qs[1]
+        if qs[0] != T or qs[2] != D:
+            raise ValueError(f"q must have shape ({T}, q_heads, {D}), got {tuple(qs)}")
         qp = _ptr(q, _BF16, dev, "q")
         if q_out is None:
-            q_out, ldqo = q.new_empty((T, Hq, D)), Hq * D
+            q_out, ldqo = _like(q), Hq * D
         else:
-            _same(q_out, (T, Hq, D), "q_out")
-            ldqo = _pitch(q_out, "q_out")
+            ldqo = _like_pitch(q_out, qs, "q_out")
         qop = _ptr(q_out, _BF16, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out is given without q")
@@ -711,14 +722,14 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     (None: T). lse fp32 [T, q_heads] receives ln sum exp of the scores when given. Returns out bf16 [T, q_heads,
     head_dim]; rows behind cu_q[batch] stay as they are."""
     dev, stream = _current(q, "q")
-    ldq = _pitch(q, "q")
-    T, Hq, D = shape = q.shape
-    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, D, dev)
+    shape = q.shape
+    ldq = _pitch(q, shape, "q")
+    T, Hq, D = shape
+    kv = _paged_kv(k_cache, v_cache, page_table, cu_q, kv_lens, None, D, dev)
     if out is None:
-        out, ldo = q.new_empty(shape), Hq * D
+        out, ldo = _like(q), Hq * D
     else:
-        _same(out, shape, "out")
-        ldo = _pitch(out, "out")
+        ldo = _like_pitch(out, shape, "out")
     lp = None
     if lse is not None:
         if lse.shape != (T, Hq) or not lse.is_contiguous():
@@ -730,7 +741,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         raise ValueError("ws must be a contiguous vector of bytes")
     _check(_lib.bf16_paged_attention(_ptr(q, _BF16, dev, "q"), ldq, T, Hq, kv, 0 if max_q is None else max_q,
                                      D ** -0.5 if scale is None else scale, window, _ptr(out, _BF16, dev, "out"), ldo,
-                                     lp, _ptr(ws, _U8, dev, "ws"), ws.shape[0], stream), "bf16_paged_attention")
+                                     lp, _ptr(ws, _U8, dev, "ws"), ws.numel(), stream), "bf16_paged_attention")
     return out
 
 

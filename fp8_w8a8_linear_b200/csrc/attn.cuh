@@ -1021,6 +1021,7 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
   uint32_t done = 0;  // key tiles so far: products with V asked for
   bool ok = true;
   int4 desc = make_int4(0, 0, 0, 0);
+  uint32_t segs = 0;
   for (bool first_seg = true; w.left > 0 && ok; first_seg = false) {
     const int m = w.seg();
     int from, to;
@@ -1064,7 +1065,7 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
         l *= f;
         mu = nm;
         if (u > from) {  // o holds the earlier keys: wait for their product
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(o_done, (done - 1) & 1, abort_w));
+          if (C::kBufs == 2) ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(o_done, (done - 1) & 1, abort_w));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -1112,7 +1113,8 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
     const int64_t tok = w.q0 + w.tok0 + tile * tt1 + rr / a.G;
     const int head = w.h * a.G + rr % a.G;
     if (to > from) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(o_done, (done - 1) & 1, abort_w));
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(o_done, (C::kBufs == 2 ? done - 1 : segs) & 1, abort_w));
+      ++segs;
       if (!ok) break;
       tc_fence_after();
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -1227,7 +1229,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
     issued = true;
   };
   // Adds the product of P, as its halves come, with V.
-  const auto product = [&](int tile, uint32_t buf, const int (&at)[PARTS], bool add) {
+  const auto product = [&](int tile, uint32_t buf, const int (&at)[PARTS], bool add, bool lastp) {
     const uint32_t b = tile * C::kBufs + buf, par = p_par >> b & 1;
     p_par ^= 1u << b;
     uint32_t vb[PARTS];
@@ -1244,7 +1246,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
                      k > 0 ? 1u : static_cast<uint32_t>(add));
       }
     }
-    umma_commit(bars + B::kODone + 8 * tile);
+    if (C::kBufs == 2 || lastp) umma_commit(bars + B::kODone + 8 * tile);
     return true;
   };
   while (w.left > 0) {
@@ -1269,7 +1271,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
         // per row tile: O += P V of this key tile, then S of the next over P
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (n >= from[i] && n < to[i] && !product(i, 0, vat, n > from[i])) return false;
+          if (n >= from[i] && n < to[i] && !product(i, 0, vat, n > from[i], n + 1 == to[i])) return false;
           if (next && n + 1 >= from[i] && n + 1 < to[i]) scores(i, 0, kat);
         }
         release(vat);
@@ -1289,7 +1291,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
           release(kat);
           if (n + 2 == m) umma_commit(bars + B::kQEmpty);
         }
-        if (!take(vat) || !product(0, buf, vat, n > 0)) return false;
+        if (!take(vat) || !product(0, buf, vat, n > 0, false)) return false;
         release(vat);
       }
     }

@@ -1487,6 +1487,13 @@ fp8_status rope_checked(const float* inv_freq, int64_t head_dim, int64_t rotary_
   return FP8_OK;
 }
 
+// Tokens per block of the rope kernels: several, so that a block's offsets,
+// pages and angles are worked out together, but one while that would leave
+// fewer than four blocks per SM (a decode step is bound by latency).
+int rope_tokens(const DeviceInfo& dev, int64_t T) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeTokens, T / (4 * dev.sm_count))));
+}
+
 // A [T, heads, D] bf16 operand with token pitch ld.
 fp8_status rows_checked(const void* p, int64_t ld, int64_t heads, int64_t D) {
   if (!p || ld < heads * D) return FP8_ERR_INVALID_ARG;
@@ -1510,9 +1517,10 @@ extern "C" fp8_status bf16_rope(const uint16_t* x, int64_t ldx, const int32_t* p
   if (!aligned4(positions)) return FP8_ERR_ALIGNMENT;
   DeviceInfo* dev;
   if (fp8_status st = device_info(&dev)) return st;
-  return launch_pdl(rope_kernel, dim3(static_cast<unsigned>(T)), dim3(kRopeThreads),
-                    as_stream(stream), x, ldx, positions, static_cast<int>(heads),
-                    static_cast<int>(head_dim), r, y, ldy);
+  const int tokens = rope_tokens(*dev, T);
+  return launch_pdl_smem(rope_kernel, dim3(static_cast<unsigned>((T + tokens - 1) / tokens)), dim3(kRopeThreads),
+                         static_cast<size_t>(tokens) * r.R * 4, as_stream(stream), x, ldx, positions,
+                         static_cast<int>(T), tokens, static_cast<int>(heads), static_cast<int>(head_dim), r, y, ldy);
 }
 
 extern "C" fp8_status bf16_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
@@ -1538,8 +1546,10 @@ extern "C" fp8_status bf16_kv_append(const uint16_t* k, int64_t ldk, const uint1
   if (fp8_status st = device_info(&dev)) return st;
   const AppendArgs a = {k, v, q, q_out, ldk, ldv, ldq, ldq_out, q ? static_cast<int>(q_heads) : 0,
                         static_cast<int>(T)};
-  return launch_pdl(kv_append_kernel, dim3(static_cast<unsigned>(T)), dim3(kRopeThreads),
-                    as_stream(stream), a, c, r);
+  const int tokens = rope_tokens(*dev, T);
+  return launch_pdl_smem(kv_append_kernel, dim3(static_cast<unsigned>((T + tokens - 1) / tokens)),
+                         dim3(kRopeThreads), static_cast<size_t>(tokens) * r.R * 4, as_stream(stream), a, c,
+                         tokens, r);
 }
 
 namespace {

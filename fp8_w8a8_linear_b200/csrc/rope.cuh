@@ -43,29 +43,34 @@ __device__ __forceinline__ void rope_angles(const RopeArgs& r, int p, float2* cs
   }
 }
 
-// A head's work comes in units: R / 16 rotating ones (eight pairs: two
-// 16-byte vectors) and (D - R) / 8 copying ones (one vector).
-__device__ __forceinline__ int rope_units(int D, int R) { return R / 16 + (D - R) / 8; }
+// A head's work comes in units of two 16-byte vectors: R / 16 rotating ones
+// (eight pairs each), then copying ones for the other D - R elements (the
+// last with one vector only when D - R is no multiple of 16). The first
+// vectors of neighbouring units lie side by side, and so do the second ones,
+// so that a warp's accesses are contiguous.
+__host__ __device__ __forceinline__ int rope_units(int D) { return (D + 15) / 16; }  // R is a multiple of 16
 
 struct RopeUnit {
   uint4 a, b;
-  int ia, ib;  // element offsets in the head; ib < 0: a copying unit
-  int pair;    // first pair of a rotating unit
+  int ia, ib;  // element offsets in the head; ib < 0: no second vector
+  bool rot;    // a rotating unit
 };
 
-__device__ __forceinline__ void rope_unit_load(RopeUnit& u, const uint16_t* head, int unit,
-                                               const RopeArgs& r) {
-  const int rot = r.R / 16;
+__device__ __forceinline__ void rope_unit_load(RopeUnit& u, const uint16_t* head, int unit, int D,
+                                               const RopeArgs& r, bool rotate) {
+  const int rot = rotate ? r.R / 16 : 0;
   if (unit < rot) {
-    u.pair = 8 * unit;
-    u.ia = r.interleaved ? 16 * unit : 8 * unit;
-    u.ib = r.interleaved ? u.ia + 8 : u.ia + r.R / 2;
-    u.b = *reinterpret_cast<const uint4*>(head + u.ib);
+    u.rot = true;
+    u.ia = 8 * unit;
+    u.ib = u.ia + r.R / 2;
   } else {
-    u.ia = r.R + 8 * (unit - rot);
-    u.ib = -1;
+    const int base = 16 * rot, second = (D - base + 15) / 16 * 8;  // elements the first vectors take
+    u.rot = false;
+    u.ia = base + 8 * (unit - rot);
+    u.ib = u.ia + second < D ? u.ia + second : -1;
   }
   u.a = *reinterpret_cast<const uint4*>(head + u.ia);
+  if (u.ib >= 0) u.b = *reinterpret_cast<const uint4*>(head + u.ib);
 }
 
 __device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float (&f)[8]) {
@@ -83,18 +88,20 @@ __device__ __forceinline__ uint4 f32_to_bf16x8(const float (&f)[8]) {
 
 __device__ __forceinline__ void rope_unit_store(RopeUnit& u, uint16_t* head, const float2* cs,
                                                 const RopeArgs& r) {
-  if (u.ib >= 0) {
+  if (u.rot) {
     float a[8], b[8];
     bf16x8_to_f32(u.a, a);
     bf16x8_to_f32(u.b, b);
-    const float4* c4 = reinterpret_cast<const float4*>(cs + u.pair);
+    // eight pairs: from ia on, or when interleaved four from ia / 2 and four from ib / 2 on
+    const float4* c4 = reinterpret_cast<const float4*>(cs + (r.interleaved ? u.ia / 2 : u.ia));
+    const float4* d4 = reinterpret_cast<const float4*>(cs + (r.interleaved ? u.ib / 2 : u.ia + 4));
     float c[8], s[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = c4[i];
+      const float4 v = i < 2 ? c4[i] : d4[i - 2];
       c[2 * i] = v.x, s[2 * i] = v.y, c[2 * i + 1] = v.z, s[2 * i + 1] = v.w;
     }
-    if (r.interleaved) {  // a: pairs 0..3 of the unit, b: pairs 4..7
+    if (r.interleaved) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float a1 = a[2 * i], a2 = a[2 * i + 1], b1 = b[2 * i], b2 = b[2 * i + 1];
@@ -113,29 +120,70 @@ __device__ __forceinline__ void rope_unit_store(RopeUnit& u, uint16_t* head, con
     }
     u.a = f32_to_bf16x8(a);
     u.b = f32_to_bf16x8(b);
-    *reinterpret_cast<uint4*>(head + u.ib) = u.b;
   }
   *reinterpret_cast<uint4*>(head + u.ia) = u.a;
+  if (u.ib >= 0) *reinterpret_cast<uint4*>(head + u.ib) = u.b;
 }
 
-// y[t, h] = x[t, h] rotated by positions[t]; one block per token. In place
-// (y == x) is sound: a unit is read whole by the thread that writes it.
+// Both kernels: a block takes a few tokens, whose rows (heads of one token
+// after the other) are dealt to groups of rope_units(D) threads; a thread has
+// the same unit in all of its rows, so it divides only once, and has
+// kRopeFlight rows in flight. The positions and angles of the block's tokens
+// are worked out once, under the first rows' loads. Bound by the bytes (one read,
+// one write).
+constexpr int kRopeFlight = 2;
+constexpr int kRopeTokens = 8;  // a block's, at most
+
+struct RopeRow {
+  int tok, row;  // row of the token
+  int by_tok, by_row, per;
+  __device__ __forceinline__ RopeRow(int first, int by, int per_) : per(per_) {
+    tok = first / per, row = first - tok * per;
+    by_tok = by / per, by_row = by - by_tok * per;
+  }
+  __device__ __forceinline__ void step() {
+    tok += by_tok;
+    row += by_row;
+    if (row >= per) row -= per, ++tok;
+  }
+};
+
+// y[t, h] = x[t, h] rotated by positions[t]. In place (y == x) is sound: a
+// unit is read whole by the thread that writes it.
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const uint16_t* x, int64_t ldx,
-                                                            const int32_t* __restrict__ positions,
-                                                            int H, int D, RopeArgs r, uint16_t* y,
-                                                            int64_t ldy) {
-  __shared__ __align__(16) float2 cs[kRopeMaxRotary / 2];
+                                                            const int32_t* __restrict__ positions, int T,
+                                                            int tokens, int H, int D, RopeArgs r,
+                                                            uint16_t* y, int64_t ldy) {
+  extern __shared__ __align__(16) float2 rope_cs[];  // [tokens][R / 2]
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t t = blockIdx.x;
-  const int units = rope_units(D, r.R), n = H * units;
-  rope_angles(r, positions[t], cs, threadIdx.x, kRopeThreads);
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kRopeThreads) {
-    const int h = i / units;
-    RopeUnit u;
-    rope_unit_load(u, x + t * ldx + static_cast<int64_t>(h) * D, i - h * units, r);
-    rope_unit_store(u, y + t * ldy + static_cast<int64_t>(h) * D, cs, r);
+  const int t0 = blockIdx.x * tokens, nt = min(tokens, T - t0);
+  const int units = rope_units(D), groups = kRopeThreads / units, group = threadIdx.x / units;
+  const int unit = threadIdx.x - group * units;
+  RopeRow w(group, groups, H);
+  if (group >= groups) w.tok = nt;  // a thread left over
+  bool first = true;
+  while (first || w.tok < nt) {
+    RopeUnit u[kRopeFlight];
+    int64_t at[kRopeFlight];
+    int tk[kRopeFlight];
+#pragma unroll
+    for (int f = 0; f < kRopeFlight; ++f) {
+      tk[f] = w.tok;
+      if (w.tok < nt) {
+        at[f] = static_cast<int64_t>(w.row) * D;
+        rope_unit_load(u[f], x + (t0 + w.tok) * ldx + at[f], unit, D, r, true);
+        w.step();
+      }
+    }
+    if (first) {
+      for (int k = 0; k < nt; ++k) rope_angles(r, positions[t0 + k], rope_cs + k * (r.R / 2), threadIdx.x, kRopeThreads);
+      __syncthreads();
+      first = false;
+    }
+#pragma unroll
+    for (int f = 0; f < kRopeFlight; ++f)
+      if (tk[f] < nt) rope_unit_store(u[f], y + (t0 + tk[f]) * ldy + at[f], rope_cs + tk[f] * (r.R / 2), r);
   }
 }
 
@@ -167,51 +215,80 @@ struct AppendArgs {
   int T;
 };
 
-// New token t of the batch: its keys (rotated) and values go to its place in
-// the cache, its queries (rotated) to q_out; one block per token. The
-// sequence is the number of offsets at or below t, counted by the block.
-__global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(AppendArgs a, PagedArgs c,
+// The new tokens' keys (rotated) and values go to their places in the cache,
+// their queries (rotated) to q_out. The sequence of a block's first token is
+// the number of offsets at or below it, counted by the block; those of its
+// other tokens follow from there.
+__global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(AppendArgs a, PagedArgs c, int tokens,
                                                                  RopeArgs r) {
-  __shared__ __align__(16) float2 cs[kRopeMaxRotary / 2];
+  extern __shared__ __align__(16) float2 rope_cs[];  // [tokens][R / 2]
+  __shared__ int64_t place[kRopeTokens];  // a token's offset in the cache; -1: it has none
+  __shared__ int where[kRopeTokens];      // its position
   pdl_launch_dependents();
   pdl_wait();
-  const int t = blockIdx.x;
-  int b = 0;
+  const int t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0);
+  int b0 = 0;
   for (int i0 = 0; i0 < c.batch; i0 += kRopeThreads) {
     const int i = i0 + threadIdx.x;
-    b += __syncthreads_count(i < c.batch && c.cu_q[min(i, c.batch - 1) + 1] <= t);
+    b0 += __syncthreads_count(i < c.batch && c.cu_q[min(i, c.batch - 1) + 1] <= t0);
   }
-  if (b >= c.batch) return;  // a row behind the last sequence
-  const int q0 = c.cu_q[b], q1 = c.cu_q[b + 1], len = c.kv_lens[b];
-  const int64_t p64 = static_cast<int64_t>(len) - q1 + t;  // len - q_len + (t - q0)
-  const bool ok = seq_ok(c, q0, q1, len, a.T) && q0 <= t && t < q1 && p64 >= 0;
-  const int p = ok ? static_cast<int>(p64) : 0;
-  const int32_t page = ok ? c.table[static_cast<int64_t>(b) * c.max_pages + p / c.page_size] : -1;
-  if (page < 0 || page >= c.num_pages) {
-    if (threadIdx.x == 0) report(FP8_DEV_BAD_INDEX);
-    return;
+  if (threadIdx.x < nt) {
+    const int t = t0 + threadIdx.x;
+    int b = b0;
+    while (b < c.batch && c.cu_q[b + 1] <= t) ++b;
+    int64_t at = -1;
+    int p = 0;
+    if (b < c.batch) {  // (else a row behind the last sequence)
+      const int q0 = c.cu_q[b], q1 = c.cu_q[b + 1], len = c.kv_lens[b];
+      const int64_t p64 = static_cast<int64_t>(len) - q1 + t;  // len - q_len + (t - q0)
+      int32_t page = -1;
+      if (seq_ok(c, q0, q1, len, a.T) && q0 <= t && t < q1 && p64 >= 0) {
+        p = static_cast<int>(p64);
+        page = c.table[static_cast<int64_t>(b) * c.max_pages + p / c.page_size];
+      }
+      if (page >= 0 && page < c.num_pages)
+        at = page * c.page_stride + (p % c.page_size) * c.token_stride;
+      else
+        report(FP8_DEV_BAD_INDEX);
+    }
+    place[threadIdx.x] = at;
+    where[threadIdx.x] = p;
   }
-  rope_angles(r, p, cs, threadIdx.x, kRopeThreads);
-  __syncthreads();
-  const int64_t slot = page * c.page_stride + (p % c.page_size) * c.token_stride;
-  const int units = rope_units(c.D, r.R), vecs = c.D / 8;
-  const int nk = c.heads * units, nq = a.Hq * units, nv = c.heads * vecs;
-  for (int i = threadIdx.x; i < nk + nq + nv; i += kRopeThreads) {
-    if (i < nk + nq) {
-      const bool key = i < nk;
-      const int j = key ? i : i - nk;
-      const int h = j / units;
-      const uint16_t* src = key ? a.k + t * a.ldk : a.q + t * a.ldq;
-      uint16_t* dst = key ? c.k + slot + h * c.head_stride
-                          : a.q_out + t * a.ldq_out + static_cast<int64_t>(h) * c.D;
-      RopeUnit u;
-      rope_unit_load(u, src + static_cast<int64_t>(h) * c.D, j - h * units, r);
-      rope_unit_store(u, dst, cs, r);
-    } else {
-      const int j = i - nk - nq;
-      const int h = j / vecs, e = 8 * (j - h * vecs);
-      *reinterpret_cast<uint4*>(c.v + slot + h * c.head_stride + e) =
-          *reinterpret_cast<const uint4*>(a.v + t * a.ldv + static_cast<int64_t>(h) * c.D + e);
+  // a token's rows: its keys, its queries, its values
+  const int units = rope_units(c.D), groups = kRopeThreads / units, group = threadIdx.x / units;
+  const int unit = threadIdx.x - group * units, nk = c.heads, nkq = c.heads + a.Hq;
+  RopeRow w(group, groups, nkq + c.heads);
+  if (group >= groups) w.tok = nt;  // a thread left over
+  bool first = true;
+  while (first || w.tok < nt) {
+    RopeUnit u[kRopeFlight];
+    int tk[kRopeFlight], row[kRopeFlight];
+#pragma unroll
+    for (int f = 0; f < kRopeFlight; ++f) {
+      tk[f] = w.tok;
+      row[f] = w.row;
+      if (w.tok < nt) {
+        const int64_t t = t0 + w.tok;
+        const uint16_t* src = w.row < nk    ? a.k + t * a.ldk + static_cast<int64_t>(w.row) * c.D
+                              : w.row < nkq ? a.q + t * a.ldq + static_cast<int64_t>(w.row - nk) * c.D
+                                            : a.v + t * a.ldv + static_cast<int64_t>(w.row - nkq) * c.D;
+        rope_unit_load(u[f], src, unit, c.D, r, w.row < nkq);
+        w.step();
+      }
+    }
+    if (first) {
+      __syncthreads();  // place, where
+      for (int k = 0; k < nt; ++k) rope_angles(r, where[k], rope_cs + k * (r.R / 2), threadIdx.x, kRopeThreads);
+      __syncthreads();
+      first = false;
+    }
+#pragma unroll
+    for (int f = 0; f < kRopeFlight; ++f) {
+      if (tk[f] >= nt || place[tk[f]] < 0) continue;
+      uint16_t* dst = row[f] < nk    ? c.k + place[tk[f]] + row[f] * c.head_stride
+                      : row[f] < nkq ? a.q_out + (t0 + tk[f]) * a.ldq_out + static_cast<int64_t>(row[f] - nk) * c.D
+                                     : c.v + place[tk[f]] + (row[f] - nkq) * c.head_stride;
+      rope_unit_store(u[f], dst, rope_cs + tk[f] * (r.R / 2), r);
     }
   }
 }
