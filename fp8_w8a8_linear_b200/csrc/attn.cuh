@@ -77,8 +77,8 @@ struct AttnRun {
   int seq;
   int units;
   int per;
-  int head, block, tile;  // where in the sequence it starts
-  long long sub_off;      // units of the sequence before it
+  int head;       // the head it starts in,
+  long long off;  // and the head's tiles before it
 };
 
 // Quotients of numbers that nearly always fit 32 bits (a 64-bit division
@@ -87,64 +87,45 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
 
-template <int THREADS>
-struct PlanSmem {
-  long long wsum[THREADS / 32];
-  AttnRun run;
-};
-
-// Finds CTA `cta`'s run of `ctas`; every thread of the block calls it. The
-// weight of a sequence is weight(b) units.
-template <int THREADS, typename Weight>
-__device__ __forceinline__ AttnRun find_run(PlanSmem<THREADS>& sm, int batch, int cta, int ctas,
-                                            Weight weight) {
-  constexpr int W = THREADS / 32;
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  // all units, and this thread's first weight (the only one when batch <= THREADS)
-  long long first = tid < batch ? weight(tid) : 0, sum = first;
-  for (int b = tid + THREADS; b < batch; b += THREADS) sum += weight(b);
+// Finds CTA `cta`'s run of `ctas`; whole warps call it, each for itself (that
+// needs no barrier: for up to 32 sequences one round of loads and a scan).
+// per_head(b) is the number of key tiles of one of sequence b's heads.
+template <typename PerHead>
+__device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int ctas, PerHead per_head) {
+  const int lane = lane_id();
+  const long long first = lane < batch ? per_head(lane) : 0;
+  long long sum = first;
+  for (int b = lane + 32; b < batch; b += 32) sum += per_head(b);
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  if (lane == 0) sm.wsum[w] = sum;
-  if (tid == 0) sm.run.units = 0;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) total += sm.wsum[i];
-  const long long per = max(1ll, div_ll(total + ctas - 1, ctas));
-  const long long start = per * cta;
-  if (start < total) {  // block-uniform
-    long long base = 0;
-    for (int b0 = 0; b0 < batch && base <= start; b0 += THREADS) {
-      const int b = b0 + tid;
-      const long long mine = b0 == 0 ? first : b < batch ? weight(b) : 0;
-      long long incl = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-        if (lane >= d) incl += v;
-      }
-      __syncthreads();  // wsum is free
-      if (lane == 31) sm.wsum[w] = incl;
-      __syncthreads();
-      long long before = base, all = 0;
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        before += i < w ? sm.wsum[i] : 0;
-        all += sm.wsum[i];
-      }
-      const long long hi = before + incl, lo = hi - mine;
-      if (lo <= start && start < hi) {
-        sm.run.seq = b;
-        sm.run.sub_off = start - lo;
-        sm.run.units = static_cast<int>(min(per, total - start));
-      }
-      base += all;
-    }
-  }
-  __syncthreads();
-  AttnRun r = sm.run;
+  sum *= heads;
+  AttnRun r;
+  r.seq = 0, r.units = 0, r.head = 0, r.off = 0;
+  const long long per = max(1ll, div_ll(sum + ctas - 1, ctas)), start = per * cta;
   r.per = static_cast<int>(per);
+  if (start >= sum) return r;
+  long long base = 0;
+  for (int b0 = 0; b0 < batch; b0 += 32) {
+    const long long tiles = b0 == 0 ? first : b0 + lane < batch ? per_head(b0 + lane) : 0, mine = tiles * heads;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    const long long lo = base + incl - mine;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, lo <= start && start < lo + mine);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const long long off = start - __shfl_sync(0xFFFFFFFFu, lo, src), n = __shfl_sync(0xFFFFFFFFu, tiles, src);
+      r.seq = b0 + src;
+      r.units = static_cast<int>(min(per, sum - start));
+      r.head = static_cast<int>(div_ll(off, n));
+      r.off = off - r.head * n;
+      return r;
+    }
+    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
   return r;
 }
 
@@ -308,7 +289,7 @@ struct RowsCfg {
   static constexpr int kXStride = 40;  // floats per row of the exchange: 32 columns, conflict-free
   static constexpr int kXBytes = 4 * kRowsMax * kXStride * 4;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(SLOTS) * kSlotBytes + kXBytes +
-                                  2 * 4 * kRowsMax * 4 + 16 * SLOTS + 16 + sizeof(PlanSmem<kRowsThreads>);
+                                  2 * 4 * kRowsMax * 4 + 16 * SLOTS + 16;
 };
 
 // 5-D tiled load (see make_tmap_paged): coordinates (0, token, 0, head, page).
@@ -355,8 +336,8 @@ struct RowsWalk {
     h = 0, t = 0;
     if (left > 0) {
       s = seq_span(a, c, b, kRowsBN);
-      h = static_cast<int>(div_ll(r.sub_off, s.tiles));
-      t = static_cast<int>(r.sub_off - static_cast<long long>(h) * s.tiles);
+      h = r.head;
+      t = static_cast<int>(r.off);
     }
   }
   __device__ __forceinline__ int seg() const { return min(left, s.tiles - t); }
@@ -388,7 +369,6 @@ __global__ void __launch_bounds__(kRowsThreads)
   float2* xml = reinterpret_cast<float2*>(xch + 4 * kRowsMax * C::kXStride);  // [4][16]
   uint64_t* bars = reinterpret_cast<uint64_t*>(xml + 4 * kRowsMax);
   uint32_t* abort_p = reinterpret_cast<uint32_t*>(bars + 2 * SLOTS);
-  auto* plan = reinterpret_cast<PlanSmem<kRowsThreads>*>(abort_p + 4);
   const uint32_t slot0 = smem_u32(smem), full0 = smem_u32(bars), empty0 = smem_u32(bars + SLOTS);
   const uint32_t abort_w = smem_u32(abort_p);
   const int warp = warp_id(), lane = lane_id();
@@ -402,13 +382,14 @@ __global__ void __launch_bounds__(kRowsThreads)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
   const int cta = blockIdx.x;
-  const AttnRun run = find_run<kRowsThreads>(*plan, c.batch, cta, gridDim.x, [&](int b) -> long long {
+  const AttnRun run = find_run(c.batch, c.heads, cta, gridDim.x, [&](int b) -> long long {
     const SeqSpan s = seq_span(a, c, b, kRowsBN);
     if (!s.ok && cta == 0) report(FP8_DEV_BAD_INDEX);
-    return static_cast<long long>(s.tiles) * c.heads;
+    return s.tiles;
   });
   RowsWalk w(a, c, run);
 
@@ -705,7 +686,7 @@ struct ChunkCfg {
   static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 2 + 2;  // see ChunkBars
   static constexpr int kWalkInts = 16;
   static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kSlots) * kSlotBytes + 8 * kBars + 16 +
-                                  sizeof(PlanSmem<kThreads>) + (kThreads / 32) * kWalkInts * 4;
+                                  (kThreads / 32) * kWalkInts * 4;
 };
 
 // sum_{i < n} floor((a i + b) / m) for a n + b < 2^32 (the Euclid-like
@@ -767,49 +748,36 @@ __device__ __forceinline__ long long chunk_tiles(int first, int len, int window,
   return s;
 }
 
-// Finds the head, block and tile at which a run starts in its sequence (the
-// whole block calls it): the blocks' tiles are added up a block per thread.
-template <int THREADS>
-__device__ __forceinline__ void find_block(PlanSmem<THREADS>& sm, AttnRun& r, const AttnArgs& a,
-                                           const PagedArgs& c, int tt) {
-  constexpr int W = THREADS / 32;
-  if (r.units <= 0) return;  // block-uniform
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+// The block of tt tokens, and the tile of it, at which a run starts in its
+// head: the blocks' tiles are added up, a block per lane (whole warps).
+__device__ __forceinline__ void find_block(const AttnRun& r, const AttnArgs& a, const PagedArgs& c, int tt, int& block,
+                                           int& tile) {
+  block = tile = 0;
+  if (r.units <= 0) return;
+  const int lane = lane_id();
   const SeqSpan s = seq_span(a, c, r.seq, kChunkBN);
-  const int first = s.len - s.ql, nb = (s.ql + tt - 1) / tt;
-  const long long per_head = chunk_tiles(first, s.len, a.window, tt, s.ql);
-  r.head = static_cast<int>(div_ll(r.sub_off, per_head));
-  const long long off = r.sub_off - r.head * per_head;
+  const int first = s.len - s.ql;
   long long base = 0;
-  for (int j0 = 0; j0 < nb && base <= off; j0 += THREADS) {
-    const int j = j0 + tid;
+  for (int j0 = 0; j0 * tt < s.ql; j0 += 32) {
+    const int tok0 = (j0 + lane) * tt;
     int tile0;
-    const int mine = j < nb ? block_tiles(first, a.window, j * tt, min(tt, s.ql - j * tt), tile0) : 0;
-    long long incl = mine;
+    const int mine = tok0 < s.ql ? block_tiles(first, a.window, tok0, min(tt, s.ql - tok0), tile0) : 0;
+    int incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
       if (lane >= d) incl += v;
     }
-    __syncthreads();  // wsum is free
-    if (lane == 31) sm.wsum[w] = incl;
-    __syncthreads();
-    long long before = base, all = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      before += i < w ? sm.wsum[i] : 0;
-      all += sm.wsum[i];
+    const long long lo = base + incl - mine;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, lo <= r.off && r.off < lo + mine);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      block = j0 + src;
+      tile = static_cast<int>(r.off - __shfl_sync(0xFFFFFFFFu, lo, src));
+      return;
     }
-    const long long hi = before + incl, lo = hi - mine;
-    if (lo <= off && off < hi) {
-      sm.run.block = j;
-      sm.run.tile = static_cast<int>(off - lo);
-    }
-    base += all;
+    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
-  __syncthreads();
-  r.block = sm.run.block;
-  r.tile = sm.run.tile;
 }
 
 // A run's segments: tiles t .. of item (sequence b, head h, block j). Each
@@ -834,9 +802,10 @@ struct ChunkWalk {
     ntok = min(ql - tok0, tt);
     n = block_tiles(first, a.window, tok0, ntok, tile0);
   }
-  __device__ __forceinline__ void start(const AttnArgs& a, const PagedArgs& c, const AttnRun& r, int tt) {
+  __device__ __forceinline__ void start(const AttnArgs& a, const PagedArgs& c, const AttnRun& r, int block, int tile,
+                                        int tt) {
     if (lane_id() == 0) {
-      b = r.seq, left = r.units, h = r.head, j = r.block, t = r.tile, g = 0;
+      b = r.seq, left = r.units, h = r.head, j = block, t = tile, g = 0;
       if (left > 0) {
         seq(a, c);
         item(a, tt);
@@ -1325,8 +1294,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + B::kEmpty, q_full = full0 + B::kQFull,
                  q_empty = full0 + B::kQEmpty, s_full = full0 + B::kSFull, p_full = full0 + B::kPFull,
                  o_done = full0 + B::kODone, v_tmp = full0 + B::kVTmp;
-  auto* plan = reinterpret_cast<PlanSmem<C::kThreads>*>(bars + C::kBars);
-  uint32_t* words = reinterpret_cast<uint32_t*>(plan + 1);
+  uint32_t* words = reinterpret_cast<uint32_t*>(bars + C::kBars);
   const uint32_t abort_w = smem_u32(words);
   uint32_t* tmem_holder = words + 1;
   static_assert(sizeof(ChunkWalk) <= C::kWalkInts * 4, "walks");
@@ -1366,14 +1334,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   pdl_launch_dependents();  // this CTA holds its TMEM
   pdl_wait();
   const int tt1 = 128 / a.G, tt = NT * tt1;
-  AttnRun run = find_run<C::kThreads>(*plan, c.batch, blockIdx.x, gridDim.x, [&](int b) -> long long {
+  const AttnRun run = find_run(c.batch, c.heads, blockIdx.x, gridDim.x, [&](int b) -> long long {
     const SeqSpan s = seq_span(a, c, b, kChunkBN);
     if (!s.ok && blockIdx.x == 0) report(FP8_DEV_BAD_INDEX);
     if (s.ql == 0) return 0;
-    return chunk_tiles(s.len - s.ql, s.len, a.window, tt, s.ql) * c.heads;
+    return chunk_tiles(s.len - s.ql, s.len, a.window, tt, s.ql);
   });
-  find_block(*plan, run, a, c, tt);
-  w.start(a, c, run, tt);
+  int block, first_tile;
+  find_block(run, a, c, tt, block, first_tile);
+  w.start(a, c, run, block, first_tile, tt);
 
   if (warp < kMmaWarp) {
     const int tile = warp >> 2;
@@ -1477,10 +1446,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     while (w.left > 0 && ok) {
       const int m = w.seg();
       const int tile = w.tile0 + w.t;
-      int2 pg = pages_of(tile);
+      int2 pg;
       if (keys) {
-        if (q_count > 0) load(pg, 0);  // under the last segment's end; the first queries come first
-        if (q_count > 0) wait(q_empty, (q_count - 1) & 1);
+        if (q_count > 0) {  // the first keys come in under the last segment's end; the first queries come first
+          load(pages_of(tile), 0);
+          wait(q_empty, (q_count - 1) & 1);
+        }
         if (ok) {
           ++q_count;
           const int nq = w.tile_tokens(1, tt1) > 0 && NT == 2 ? 2 : 1;
@@ -1492,10 +1463,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
             tma_load_q(q_smem + i * (128 * D * 2) + qg * 16384, &tmQ, q_full, w.h * a.G,
                        w.q0 + w.tok0 + i * tt1, qg);
           }
-          if (q_count == 1) load(pg, 0);
+          if (q_count == 1) load(pages_of(tile), 0);
         }
         // order: K0 V0 K1 V1 ..., with two buffers for S K0 K1 V0 K2 V1 ...
-        int2 pg_next = m > 1 ? pages_of(tile + 1) : pg;
+        int2 pg_next = m > 1 ? pages_of(tile + 1) : make_int2(-2, 0);
         for (int n = 0; n < m && ok; ++n) {
           pg = pg_next;
           if (n + 2 < m) pg_next = pages_of(tile + n + 2);
@@ -1504,6 +1475,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           if (NT == 1) skip();
         }
       } else {
+        pg = pages_of(tile);
         skip();
         for (int n = 0; n < m && ok; ++n) {
           const int2 pg_next = n + 1 < m ? pages_of(tile + n + 1) : make_int2(-2, 0);
