@@ -71,14 +71,15 @@ __device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, const PagedArgs& 
   return s;
 }
 
-// A CTA's run: `units` key tiles from one of sequence `seq`'s on; `per` is
-// the length of a full run.
+// A CTA's run: the key tiles that start in `units` units from one of sequence
+// `seq`'s on (a tile is one unit long, or two); `per` is the length of a full
+// run.
 struct AttnRun {
   int seq;
   int units;
   int per;
   int head;       // the head it starts in,
-  long long off;  // and the head's tiles before it
+  long long off;  // and the head's units before it
 };
 
 // Quotients of numbers that nearly always fit 32 bits (a 64-bit division
@@ -89,9 +90,12 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
 
 // Finds CTA `cta`'s run of `ctas`; whole warps call it, each for itself (that
 // needs no barrier: for up to 32 sequences one round of loads and a scan).
-// per_head(b) is the number of key tiles of one of sequence b's heads.
+// per_head(b) is the length of one of sequence b's heads' key tiles; it sets
+// `wide` if some are two units long (a run is then no shorter, so that every
+// run inside an item holds a tile of it).
 template <typename PerHead>
-__device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int ctas, PerHead per_head) {
+__device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int ctas, const bool& wide,
+                                            PerHead per_head) {
   const int lane = lane_id();
   const long long first = lane < batch ? per_head(lane) : 0;
   long long sum = first;
@@ -101,7 +105,7 @@ __device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int c
   sum *= heads;
   AttnRun r;
   r.seq = 0, r.units = 0, r.head = 0, r.off = 0;
-  const long long per = max(1ll, div_ll(sum + ctas - 1, ctas)), start = per * cta;
+  const long long per = max(__any_sync(0xFFFFFFFFu, wide) ? 2ll : 1ll, div_ll(sum + ctas - 1, ctas)), start = per * cta;
   r.per = static_cast<int>(per);
   if (start >= sum) return r;
   long long base = 0;
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kRowsThreads)
   pdl_launch_dependents();
   pdl_wait();
   const int cta = blockIdx.x;
-  const AttnRun run = find_run(c.batch, c.heads, cta, gridDim.x, [&](int b) -> long long {
+  const AttnRun run = find_run(c.batch, c.heads, cta, gridDim.x, false, [&](int b) -> long long {
     const SeqSpan s = seq_span(a, c, b, kRowsBN);
     if (!s.ok && cta == 0) report(FP8_DEV_BAD_INDEX);
     return s.tiles;
@@ -683,10 +687,10 @@ struct ChunkCfg {
   static constexpr int kQBytes = kNT * 128 * D * 2;
   static constexpr int kThreads = kNT * 128 + 128;
   static constexpr int kRows = kNT * 128;            // rows of a part in the workspace
-  static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 2 + 2;  // see ChunkBars
+  static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 2 + 2 + 2;  // see ChunkBars
   static constexpr int kWalkInts = 16;
   static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kSlots) * kSlotBytes + 8 * kBars + 16 +
-                                  (kThreads / 32) * kWalkInts * 4;
+                                  (kThreads / 32) * kWalkInts * 4 + (kNT == 2 ? 128 * 8 : 0);
 };
 
 // sum_{i < n} floor((a i + b) / m) for a n + b < 2^32 (the Euclid-like
@@ -748,11 +752,15 @@ __device__ __forceinline__ long long chunk_tiles(int first, int len, int window,
   return s;
 }
 
-// The block of tt tokens, and the tile of it, at which a run starts in its
-// head: the blocks' tiles are added up, a block per lane (whole warps).
-__device__ __forceinline__ void find_block(const AttnRun& r, const AttnArgs& a, const PagedArgs& c, int tt, int& block,
-                                           int& tile) {
-  block = tile = 0;
+// Units that a key tile of ntok tokens' rows counts for: two row tiles cost
+// about twice what one does.
+__device__ __forceinline__ int tile_units(int ntok, int tt1) { return ntok > tt1 ? 2 : 1; }
+
+// The block of tt tokens at which a run starts in its head, and how far into
+// it: the blocks' units are added up, a block per lane (whole warps).
+__device__ __forceinline__ void find_block(const AttnRun& r, const AttnArgs& a, const PagedArgs& c, int tt, int tt1,
+                                           int& block, int& unit) {
+  block = unit = 0;
   if (r.units <= 0) return;
   const int lane = lane_id();
   const SeqSpan s = seq_span(a, c, r.seq, kChunkBN);
@@ -761,7 +769,8 @@ __device__ __forceinline__ void find_block(const AttnRun& r, const AttnArgs& a, 
   for (int j0 = 0; j0 * tt < s.ql; j0 += 32) {
     const int tok0 = (j0 + lane) * tt;
     int tile0;
-    const int mine = tok0 < s.ql ? block_tiles(first, a.window, tok0, min(tt, s.ql - tok0), tile0) : 0;
+    const int ntok = min(tt, s.ql - tok0);
+    const int mine = ntok > 0 ? block_tiles(first, a.window, tok0, ntok, tile0) * tile_units(ntok, tt1) : 0;
     int incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -773,7 +782,7 @@ __device__ __forceinline__ void find_block(const AttnRun& r, const AttnArgs& a, 
     if (hit) {
       const int src = __ffs(hit) - 1;
       block = j0 + src;
-      tile = static_cast<int>(r.off - __shfl_sync(0xFFFFFFFFu, lo, src));
+      unit = static_cast<int>(r.off - __shfl_sync(0xFFFFFFFFu, lo, src));
       return;
     }
     base += __shfl_sync(0xFFFFFFFFu, incl, 31);
@@ -802,21 +811,31 @@ struct ChunkWalk {
     ntok = min(ql - tok0, tt);
     n = block_tiles(first, a.window, tok0, ntok, tile0);
   }
-  __device__ __forceinline__ void start(const AttnArgs& a, const PagedArgs& c, const AttnRun& r, int block, int tile,
-                                        int tt) {
+  __device__ __forceinline__ void start(const AttnArgs& a, const PagedArgs& c, const AttnRun& r, int block, int unit,
+                                        int tt, int tt1) {
     if (lane_id() == 0) {
-      b = r.seq, left = r.units, h = r.head, j = block, t = tile, g = 0;
+      b = r.seq, left = r.units, h = r.head, j = block, t = 0, g = 0;
       if (left > 0) {
         seq(a, c);
         item(a, tt);
+        const int wt = tile_units(ntok, tt1);
+        t = (unit + wt - 1) / wt;  // the first tile that starts in the run
+        left -= t * wt - unit;
+        if (t == n) advance(a, c, 0, tt, tt1);
       }
     }
     __syncwarp();
   }
-  __device__ __forceinline__ int seg() const { return min(left, n - t); }
+  __device__ __forceinline__ int seg(int tt1) const {
+    return min(ntok > tt1 ? (left + 1) >> 1 : left, n - t);
+  }
+  // The runs after this one that hold a part of the item, whose first tile is next.
+  __device__ __forceinline__ int more(int per, int tt1) const {
+    return (per - left + (n - 1) * tile_units(ntok, tt1)) / per;
+  }
   // Past m tiles (one thread).
-  __device__ __forceinline__ void advance(const AttnArgs& a, const PagedArgs& c, int m, int tt) {
-    left -= m;
+  __device__ __forceinline__ void advance(const AttnArgs& a, const PagedArgs& c, int m, int tt, int tt1) {
+    left -= m * tile_units(ntok, tt1);
     g += m;
     t = 0;
     if (left <= 0) return;
@@ -835,9 +854,9 @@ struct ChunkWalk {
     }
     item(a, tt);
   }
-  __device__ __forceinline__ void next(const AttnArgs& a, const PagedArgs& c, int m, int tt) {
+  __device__ __forceinline__ void next(const AttnArgs& a, const PagedArgs& c, int m, int tt, int tt1) {
     __syncwarp();
-    if (lane_id() == 0) advance(a, c, m, tt);
+    if (lane_id() == 0) advance(a, c, m, tt, tt1);
     __syncwarp();
   }
   // Row tile i (tt1 tokens each): its tokens, and those of the segment's m key
@@ -980,7 +999,8 @@ __device__ __forceinline__ void chunk_probs(const uint32_t (&s)[64], float scale
 template <int D>
 __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs& c, ChunkWalk& w, int tile,
                                               int tt1, uint32_t tmem, uint32_t s_full, uint32_t p_full,
-                                              uint32_t o_done, uint32_t abort_w, int per) {
+                                              uint32_t o_done, uint32_t ml_full, float2* ml, uint32_t abort_w,
+                                              int per) {
   using C = ChunkCfg<D>;
   const int lane = lane_id(), quad = warp_id() & 3;
   const int rr = 32 * quad + lane;  // row of the tile
@@ -990,22 +1010,32 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
   uint32_t done = 0;  // key tiles so far: products with V asked for
   bool ok = true;
   int4 desc = make_int4(0, 0, 0, 0);
-  uint32_t segs = 0;
+  uint32_t segs = 0, joins = 0;
   for (bool first_seg = true; w.left > 0 && ok; first_seg = false) {
-    const int m = w.seg();
+    const int m = w.seg(tt1);
+    const bool turns = C::kNT == 2 && w.ntok <= tt1;  // both groups on row tile 0
+    const bool join = turns && m > 1;
+    const int rt = turns ? 0 : tile, step = turns ? 2 : 1;
     int from, to;
-    w.tile_range(a, tile, tt1, m, from, to);
-    const int ntok = w.tile_tokens(tile, tt1);
-    const int p0 = w.first + w.tok0 + tile * tt1;  // positions p0 .. p0 + ntok - 1
+    w.tile_range(a, rt, tt1, m, from, to);
+    if (turns) from += tile;
+    const int ntok = w.tile_tokens(rt, tt1);
+    const bool idle = 32 * quad >= ntok * a.G;     // this warp has no row
+    const int p0 = w.first + w.tok0 + rt * tt1;    // positions p0 .. p0 + ntok - 1
     const int key_seg = (w.tile0 + w.t) * kChunkBN;
     const int rel0 = p0 + rr / a.G - key_seg;      // this row's position, from the segment's first key
     float mu = -INFINITY, l = 0.0f;
-    for (int u = from; u < to && ok; ++u) {
+    for (int u = from; u < to; u += step) {
       const uint32_t buf = C::kBufs == 2 ? done & 1 : 0;
       const uint32_t s_addr = s_addr0 + buf * kChunkBN;
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(s_full + 8 * buf, (C::kBufs == 2 ? done >> 1 : done) & 1, abort_w));
       if (!ok) break;
       tc_fence_after();
+      if (C::kBufs == 1 && idle) {  // P keeps what it holds: nothing reads those rows of o
+        if (lane == 0) mbar_arrive(p_full), mbar_arrive(p_full + 8);
+        ++done;
+        continue;
+      }
       const int key0 = key_seg + kChunkBN * u;
       const bool edge = key0 + kChunkBN - 1 > p0 || p0 + ntok - 1 - key0 >= a.window;
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1075,17 +1105,53 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
     }
     if (!ok) break;
     // ---- the segment's o
-    const bool whole = w.t == 0 && m == w.n;
-    const int part = 2 * cta + (first_seg ? 0 : 1);
-    const bool live = rr < ntok * a.G;  // ntok <= tt1
-    const int row = tile * tt1 * a.G + rr;
-    const int64_t tok = w.q0 + w.tok0 + tile * tt1 + rr / a.G;
-    const int head = w.h * a.G + rr % a.G;
     if (to > from) {
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(o_done, (C::kBufs == 2 ? done - 1 : segs) & 1, abort_w));
       ++segs;
       if (!ok) break;
       tc_fence_after();
+    }
+    // Two groups on one row tile: the second leaves its rows' statistics in
+    // shared memory, the first reads them and both groups' o (its lanes of
+    // TMEM are the same) and goes on alone.
+    float f0 = 1.0f, f1 = 0.0f;
+    if (join) {
+      if (tile == 1) {
+        ml[rr] = make_float2(mu, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_full);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(ml_full + 8, joins & 1, abort_w));  // read
+      } else {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(ml_full, joins & 1, abort_w));
+        const float2 x = ml[rr];
+        const float mm = fmaxf(mu, x.x), mb = mm == -INFINITY ? 0.0f : mm;
+        f0 = ex2(mu - mb);
+        f1 = ex2(x.x - mb);
+        mu = mm;
+        l = l * f0 + x.y * f1;
+      }
+      ++joins;
+      if (!ok) break;
+    }
+    const bool whole = w.t == 0 && m == w.n;
+    const int part = 2 * cta + (first_seg ? 0 : 1);
+    const bool live = rr < ntok * a.G && !(turns && tile == 1);  // ntok <= tt1
+    const int row = rt * tt1 * a.G + rr;
+    const int64_t tok = w.q0 + w.tok0 + rt * tt1 + rr / a.G;
+    const int head = w.h * a.G + rr % a.G;
+    const auto load_o = [&](int cb, uint32_t (&o)[32]) {
+      tmem_ld32(o_addr + cb, o);
+      tmem_ld_wait();
+      if (C::kNT == 2 && join) {
+        uint32_t o1[32];
+        tmem_ld32(o_addr + D + cb, o1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 + __uint_as_float(o1[e]) * f1);
+      }
+    };
+    if (to > from && !idle && !(turns && tile == 1)) {
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
       if (whole) {
         // Four lanes turn their rows' 16-byte pieces among themselves, so that
@@ -1097,8 +1163,7 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
 #pragma unroll 1
         for (int cb = 0; cb < D; cb += 32) {
           uint32_t o[32], u[4][4];
-          tmem_ld32(o_addr + cb, o);
-          tmem_ld_wait();
+          load_o(cb, o);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -1115,8 +1180,7 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
 #pragma unroll 1
         for (int cb = 0; cb < D; cb += 32) {
           uint32_t o[32];
-          tmem_ld32(o_addr + cb, o);
-          tmem_ld_wait();
+          load_o(cb, o);
           if (live)
 #pragma unroll
             for (int q = 0; q < 8; ++q)
@@ -1124,7 +1188,11 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
                                                          __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
         }
       }
-      tc_fence_before();
+    }
+    tc_fence_before();
+    if (join && tile == 0) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ml_full + 8);
     }
     if (live) {
       if (!whole)
@@ -1133,21 +1201,22 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
         a.lse[tok * a.Hq + head] = l > 0.0f ? (mu + log2f(l)) * kLn2 : -INFINITY;
     }
     if (w.t == 0 && !whole)
-      desc = join_desc((w.n - m + per - 1) / per, part, w.q0 + w.tok0, w.h * a.G, w.ntok * a.G);
-    w.next(a, c, m, C::kNT * tt1);
+      desc = join_desc(w.more(per, tt1), part, w.q0 + w.tok0, w.h * a.G, w.ntok * a.G);
+    w.next(a, c, m, C::kNT * tt1, tt1);
   }
   if (tile == 0 && rr == 0) a.part_desc[cta] = ok ? desc : make_int4(0, 0, 0, 0);
 }
 
 // Barriers of the chunk kernel, by their addresses' offsets: full[kSlots],
 // empty[kSlots], queries full and empty, S full (per buffer), P full (two
-// halves per buffer), O done (per row tile), the V loader's own, drained.
+// halves per buffer), O done (per row tile), the V loader's own, drained, the
+// second softmax group's statistics there and read.
 template <int D>
 struct ChunkBars {
   using C = ChunkCfg<D>;
   static constexpr uint32_t kEmpty = 8 * C::kSlots, kQFull = 16 * C::kSlots, kQEmpty = kQFull + 8, kSFull = kQFull + 16,
-                            kPFull = kSFull + 16, kODone = kPFull + 32, kVTmp = kODone + 16, kDrained = kVTmp + 8;
-  static_assert(kDrained + 8 == 8 * C::kBars, "barriers");
+                            kPFull = kSFull + 16, kODone = kPFull + 32, kVTmp = kODone + 16, kDrained = kVTmp + 8, kMlFull = kDrained + 8, kMlEmpty = kMlFull + 8;
+  static_assert(kMlEmpty + 8 == 8 * C::kBars, "barriers");
 };
 
 // The MMAs, issued by one thread. It shares its scheduler and instruction
@@ -1182,7 +1251,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
     for (int p = 0; p < PARTS; ++p) umma_commit(bars + B::kEmpty + 8 * at[p]);
   };
   // S of a key tile for row tile `tile` into its buffer `buf`.
-  const auto scores = [&](int tile, uint32_t buf, const int (&at)[PARTS]) {
+  const auto scores = [&](int tile, int q_tile, uint32_t buf, const int (&at)[PARTS]) {
     const uint32_t b = tile * C::kBufs + buf;
     uint32_t kb[PARTS];
 #pragma unroll
@@ -1191,7 +1260,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
     for (int k = 0; k < D / 16; ++k) {
       const int p = k * 16 / C::kKCols, kk = k - p * (C::kKCols / 16);
       umma_kind<kKindBF16>(tmem + b * kChunkBN,
-                           desc_of(q_lo + (tile * (128 * D * 2) + (k >> 2) * 16384 + (k & 3) * 32) / 16),
+                           desc_of(q_lo + (q_tile * (128 * D * 2) + (k >> 2) * 16384 + (k & 3) * 32) / 16),
                            desc_of(kb[p] + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16), kIdescS, k > 0);
     }
     umma_commit(bars + B::kSFull + 8 * b);
@@ -1219,7 +1288,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
     return true;
   };
   while (w.left > 0) {
-    const int m = w.seg();
+    const int m = w.seg(tt1);
     int from[NT], to[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) w.tile_range(a, i, tt1, m, from[i], to[i]);
@@ -1228,10 +1297,26 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
     q_par ^= 1;
     if (!take(kat)) return false;
     tc_fence_after();
-    if constexpr (NT == 2) {
+    if (NT == 2 && w.ntok <= tt1) {
+      // one row tile: the two softmax groups take the key tiles in turn
+      for (int n = -2; n < m; ++n) {
+        const int i = n & 1;
+        if (n >= 0) {
+          if (!take(vat) || !product(i, 0, vat, n > 1, n + 2 >= m)) return false;
+          release(vat);
+        }
+        if (n + 2 < m) {
+          if (n > -2 && !take(kat)) return false;
+          tc_fence_after();
+          scores(i, 0, 0, kat);
+          release(kat);
+        }
+        if (n + 3 == m) umma_commit(bars + B::kQEmpty);
+      }
+    } else if constexpr (NT == 2) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (from[i] == 0 && to[i] > 0) scores(i, 0, kat);
+        if (from[i] == 0 && to[i] > 0) scores(i, i, 0, kat);
       release(kat);
       if (m == 1) umma_commit(bars + B::kQEmpty);
       for (int n = 0; n < m; ++n) {
@@ -1241,14 +1326,14 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (n >= from[i] && n < to[i] && !product(i, 0, vat, n > from[i], n + 1 == to[i])) return false;
-          if (next && n + 1 >= from[i] && n + 1 < to[i]) scores(i, 0, kat);
+          if (next && n + 1 >= from[i] && n + 1 < to[i]) scores(i, i, 0, kat);
         }
         release(vat);
         if (next) release(kat);
         if (n + 2 == m) umma_commit(bars + B::kQEmpty);
       }
     } else {
-      scores(0, w.g & 1, kat);
+      scores(0, 0, w.g & 1, kat);
       release(kat);
       if (m == 1) umma_commit(bars + B::kQEmpty);
       for (int n = 0; n < m; ++n) {
@@ -1256,7 +1341,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
         if (n + 1 < m) {
           if (!take(kat)) return false;
           tc_fence_after();
-          scores(0, buf ^ 1, kat);
+          scores(0, 0, buf ^ 1, kat);
           release(kat);
           if (n + 2 == m) umma_commit(bars + B::kQEmpty);
         }
@@ -1264,7 +1349,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
         release(vat);
       }
     }
-    w.advance(a, c, m, NT * tt1);
+    w.advance(a, c, m, NT * tt1, tt1);
   }
   return true;
 }
@@ -1299,6 +1384,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   uint32_t* tmem_holder = words + 1;
   static_assert(sizeof(ChunkWalk) <= C::kWalkInts * 4, "walks");
   auto& w = *reinterpret_cast<ChunkWalk*>(words + 4 + C::kWalkInts * warp_id());
+  auto* ml = reinterpret_cast<float2*>(words + 4 + C::kWalkInts * (C::kThreads / 32));
   const uint32_t q_smem = smem_u32(smem), slot0 = smem_u32(slots);
   const int warp = warp_id(), lane = lane_id();
   constexpr int kMmaWarp = NT * 4, kLoadWarp = NT * 4 + 1;  // and kLoadWarp + 1
@@ -1313,6 +1399,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     mbar_init(q_empty, 1);
     mbar_init(v_tmp, 1);
     mbar_init(full0 + B::kDrained, 1);
+    mbar_init(full0 + B::kMlFull, 4);
+    mbar_init(full0 + B::kMlEmpty, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(o_done + 8 * i, 1);
@@ -1334,20 +1422,26 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   pdl_launch_dependents();  // this CTA holds its TMEM
   pdl_wait();
   const int tt1 = 128 / a.G, tt = NT * tt1;
-  const AttnRun run = find_run(c.batch, c.heads, blockIdx.x, gridDim.x, [&](int b) -> long long {
+  bool wide = false;
+  const AttnRun run = find_run(c.batch, c.heads, blockIdx.x, gridDim.x, wide, [&](int b) -> long long {
     const SeqSpan s = seq_span(a, c, b, kChunkBN);
     if (!s.ok && blockIdx.x == 0) report(FP8_DEV_BAD_INDEX);
     if (s.ql == 0) return 0;
-    return chunk_tiles(s.len - s.ql, s.len, a.window, tt, s.ql);
+    const long long tiles = chunk_tiles(s.len - s.ql, s.len, a.window, tt, s.ql);
+    if (NT == 1 || s.ql <= tt1) return tiles;
+    wide = true;
+    int tile0;  // a last block of one row tile counts once
+    const int last = s.ql - (s.ql - 1) / tt * tt;
+    return 2 * tiles - (last <= tt1 ? block_tiles(s.len - s.ql, a.window, s.ql - last, last, tile0) : 0);
   });
-  int block, first_tile;
-  find_block(run, a, c, tt, block, first_tile);
-  w.start(a, c, run, block, first_tile, tt);
+  int block, unit;
+  find_block(run, a, c, tt, tt1, block, unit);
+  w.start(a, c, run, block, unit, tt, tt1);
 
   if (warp < kMmaWarp) {
     const int tile = warp >> 2;
-    chunk_softmax<D>(a, c, w, tile, tt1, tmem, s_full + 8 * tile, p_full + 16 * tile, o_done + 8 * tile, abort_w,
-                     run.per);
+    chunk_softmax<D>(a, c, w, tile, tt1, tmem, s_full + 8 * tile, p_full + 16 * tile, o_done + 8 * tile,
+                     full0 + B::kMlFull, ml, abort_w, run.per);
   } else if (warp == kMmaWarp) {
     if (lane == 0) chunk_issue<D>(a, c, w, tt1, tmem, q_smem, slot0, full0, abort_w);
   } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
@@ -1444,7 +1538,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       for (int p = 0; p < PARTS; ++p) pass();
     };
     while (w.left > 0 && ok) {
-      const int m = w.seg();
+      const int m = w.seg(tt1);
       const int tile = w.tile0 + w.t;
       int2 pg;
       if (keys) {
@@ -1465,27 +1559,29 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           }
           if (q_count == 1) load(pages_of(tile), 0);
         }
-        // order: K0 V0 K1 V1 ..., with two buffers for S K0 K1 V0 K2 V1 ...
+        // order: K0 V0 K1 V1 ..., with one row tile K0 K1 V0 K2 V1 ...
+        const bool ahead = NT == 1 || w.ntok <= tt1;
         int2 pg_next = m > 1 ? pages_of(tile + 1) : make_int2(-2, 0);
         for (int n = 0; n < m && ok; ++n) {
           pg = pg_next;
           if (n + 2 < m) pg_next = pages_of(tile + n + 2);
-          if (NT == 2) skip();
+          if (!ahead) skip();
           if (n + 1 < m) load(pg, 0);
-          if (NT == 1) skip();
+          if (ahead) skip();
         }
       } else {
+        const bool ahead = NT == 1 || w.ntok <= tt1;
         pg = pages_of(tile);
         skip();
         for (int n = 0; n < m && ok; ++n) {
           const int2 pg_next = n + 1 < m ? pages_of(tile + n + 1) : make_int2(-2, 0);
-          if (NT == 1 && n + 1 < m) skip();
+          if (ahead && n + 1 < m) skip();
           load(pg, (tile + n) * kChunkBN);
-          if (NT == 2 && n + 1 < m) skip();
+          if (!ahead && n + 1 < m) skip();
           pg = pg_next;
         }
       }
-      w.next(a, c, m, tt);
+      w.next(a, c, m, tt, tt1);
     }
     if (!ok && lane == 0) {
       // every copy started is waited for (bounded) before the CTA can exit
