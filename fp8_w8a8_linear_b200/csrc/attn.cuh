@@ -72,12 +72,14 @@ __device__ __forceinline__ SeqSpan seq_span(const AttnArgs& a, const PagedArgs& 
 }
 
 // A CTA's run: the key tiles that start in `units` units from one of sequence
-// `seq`'s on (a tile is one unit long, or two); `per` is the length of a full
-// run.
+// `seq`'s on; `per` is the length of a full run. A tile is one unit long, or
+// two, and an item's first one `extra` units more (what an item costs besides
+// its tiles).
 struct AttnRun {
   int seq;
   int units;
   int per;
+  int extra;
   int head;       // the head it starts in,
   long long off;  // and the head's units before it
 };
@@ -88,29 +90,52 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
 
+constexpr int kExtraRun = 8;  // units of a run from which on items count their own cost
+
+// A head's key tiles, in units, and its items.
+struct HeadUnits {
+  long long units;
+  int items;
+  bool wide;  // some tiles are two units long
+};
+
 // Finds CTA `cta`'s run of `ctas`; whole warps call it, each for itself (that
 // needs no barrier: for up to 32 sequences one round of loads and a scan).
-// per_head(b) is the length of one of sequence b's heads' key tiles; it sets
-// `wide` if some are two units long (a run is then no shorter, so that every
-// run inside an item holds a tile of it).
+// per_head(b): one of sequence b's heads. Items count `extra` units more
+// where the runs are long enough for that to be the smaller error; a run is
+// never shorter than the distance of two tiles' starts, so that every run
+// inside an item holds a tile of it.
 template <typename PerHead>
-__device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int ctas, const bool& wide,
-                                            PerHead per_head) {
+__device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int ctas, int extra, PerHead per_head) {
   const int lane = lane_id();
-  const long long first = lane < batch ? per_head(lane) : 0;
-  long long sum = first;
-  for (int b = lane + 32; b < batch; b += 32) sum += per_head(b);
+  HeadUnits first = {0, 0, false};
+  if (lane < batch) first = per_head(lane);
+  long long sum = first.units, items = first.items;
+  bool wide = first.wide;
+  for (int b = lane + 32; b < batch; b += 32) {
+    const HeadUnits u = per_head(b);
+    sum += u.units, items += u.items, wide |= u.wide;
+  }
 #pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  sum *= heads;
+  for (int d = 16; d; d >>= 1) {
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    items += __shfl_xor_sync(0xFFFFFFFFu, items, d);
+  }
+  sum *= heads, items *= heads;
+  if (sum < static_cast<long long>(kExtraRun) * ctas) extra = 0;
+  sum += items * extra;
   AttnRun r;
-  r.seq = 0, r.units = 0, r.head = 0, r.off = 0;
+  r.seq = 0, r.units = 0, r.head = 0, r.off = 0, r.extra = extra;
   const long long per = max(__any_sync(0xFFFFFFFFu, wide) ? 2ll : 1ll, div_ll(sum + ctas - 1, ctas)), start = per * cta;
   r.per = static_cast<int>(per);
   if (start >= sum) return r;
   long long base = 0;
   for (int b0 = 0; b0 < batch; b0 += 32) {
-    const long long tiles = b0 == 0 ? first : b0 + lane < batch ? per_head(b0 + lane) : 0, mine = tiles * heads;
+    if (b0 > 0) {
+      first = {0, 0, false};
+      if (b0 + lane < batch) first = per_head(b0 + lane);
+    }
+    const long long units = first.units + static_cast<long long>(first.items) * extra, mine = units * heads;
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -121,7 +146,7 @@ __device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int c
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, lo <= start && start < lo + mine);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      const long long off = start - __shfl_sync(0xFFFFFFFFu, lo, src), n = __shfl_sync(0xFFFFFFFFu, tiles, src);
+      const long long off = start - __shfl_sync(0xFFFFFFFFu, lo, src), n = __shfl_sync(0xFFFFFFFFu, units, src);
       r.seq = b0 + src;
       r.units = static_cast<int>(min(per, sum - start));
       r.head = static_cast<int>(div_ll(off, n));
@@ -390,10 +415,10 @@ __global__ void __launch_bounds__(kRowsThreads)
   pdl_launch_dependents();
   pdl_wait();
   const int cta = blockIdx.x;
-  const AttnRun run = find_run(c.batch, c.heads, cta, gridDim.x, false, [&](int b) -> long long {
+  const AttnRun run = find_run(c.batch, c.heads, cta, gridDim.x, 0, [&](int b) -> HeadUnits {
     const SeqSpan s = seq_span(a, c, b, kRowsBN);
     if (!s.ok && cta == 0) report(FP8_DEV_BAD_INDEX);
-    return s.tiles;
+    return {s.tiles, 0, false};
   });
   RowsWalk w(a, c, run);
 
@@ -688,6 +713,7 @@ struct ChunkCfg {
   static constexpr int kThreads = kNT * 128 + 128;
   static constexpr int kRows = kNT * 128;            // rows of a part in the workspace
   static constexpr int kBars = 2 * kSlots + 2 + 2 + 4 + 2 + 2 + 2;  // see ChunkBars
+  static constexpr int kItemUnits = D == 256 ? 2 : 3;  // what an item costs besides its tiles, in units
   static constexpr int kWalkInts = 16;
   static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kSlots) * kSlotBytes + 8 * kBars + 16 +
                                   (kThreads / 32) * kWalkInts * 4 + (kNT == 2 ? 128 * 8 : 0);
@@ -770,7 +796,7 @@ __device__ __forceinline__ void find_block(const AttnRun& r, const AttnArgs& a, 
     const int tok0 = (j0 + lane) * tt;
     int tile0;
     const int ntok = min(tt, s.ql - tok0);
-    const int mine = ntok > 0 ? block_tiles(first, a.window, tok0, ntok, tile0) * tile_units(ntok, tt1) : 0;
+    const int mine = ntok > 0 ? block_tiles(first, a.window, tok0, ntok, tile0) * tile_units(ntok, tt1) + r.extra : 0;
     int incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -798,6 +824,7 @@ struct ChunkWalk {
   int lo_seq;              // keys below it no new token sees
   int tok0, ntok, tile0, n;  // the item: tokens tok0 .. of the sequence, key tiles tile0 .. + n
   uint32_t g;                // key tiles walked so far
+  int extra;
 
   __device__ __forceinline__ bool seq(const AttnArgs& a, const PagedArgs& c) {
     const SeqSpan s = seq_span(a, c, b, kChunkBN);
@@ -814,28 +841,31 @@ struct ChunkWalk {
   __device__ __forceinline__ void start(const AttnArgs& a, const PagedArgs& c, const AttnRun& r, int block, int unit,
                                         int tt, int tt1) {
     if (lane_id() == 0) {
-      b = r.seq, left = r.units, h = r.head, j = block, t = 0, g = 0;
+      b = r.seq, left = r.units, h = r.head, j = block, t = 0, g = 0, extra = r.extra;
       if (left > 0) {
         seq(a, c);
         item(a, tt);
-        const int wt = tile_units(ntok, tt1);
-        t = (unit + wt - 1) / wt;  // the first tile that starts in the run
-        left -= t * wt - unit;
-        if (t == n) advance(a, c, 0, tt, tt1);
+        if (unit > 0) {  // the first tile that starts in the run
+          const int wt = tile_units(ntok, tt1);
+          t = max(1, (unit - extra + wt - 1) / wt);
+          left -= extra + t * wt - unit;
+          if (t == n) advance(a, c, 0, tt, tt1);
+        }
       }
     }
     __syncwarp();
   }
   __device__ __forceinline__ int seg(int tt1) const {
-    return min(ntok > tt1 ? (left + 1) >> 1 : left, n - t);
+    const int x = t == 0 ? max(1, left - extra) : left;
+    return min(ntok > tt1 ? (x + 1) >> 1 : x, n - t);
   }
   // The runs after this one that hold a part of the item, whose first tile is next.
   __device__ __forceinline__ int more(int per, int tt1) const {
-    return (per - left + (n - 1) * tile_units(ntok, tt1)) / per;
+    return n == 1 ? 0 : (per - left + extra + (n - 1) * tile_units(ntok, tt1)) / per;
   }
   // Past m tiles (one thread).
   __device__ __forceinline__ void advance(const AttnArgs& a, const PagedArgs& c, int m, int tt, int tt1) {
-    left -= m * tile_units(ntok, tt1);
+    left -= m * tile_units(ntok, tt1) + (t == 0 ? extra : 0);
     g += m;
     t = 0;
     if (left <= 0) return;
@@ -1422,17 +1452,16 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   pdl_launch_dependents();  // this CTA holds its TMEM
   pdl_wait();
   const int tt1 = 128 / a.G, tt = NT * tt1;
-  bool wide = false;
-  const AttnRun run = find_run(c.batch, c.heads, blockIdx.x, gridDim.x, wide, [&](int b) -> long long {
+  const AttnRun run = find_run(c.batch, c.heads, blockIdx.x, gridDim.x, C::kItemUnits, [&](int b) -> HeadUnits {
     const SeqSpan s = seq_span(a, c, b, kChunkBN);
     if (!s.ok && blockIdx.x == 0) report(FP8_DEV_BAD_INDEX);
-    if (s.ql == 0) return 0;
+    if (s.ql == 0) return {0, 0, false};
     const long long tiles = chunk_tiles(s.len - s.ql, s.len, a.window, tt, s.ql);
-    if (NT == 1 || s.ql <= tt1) return tiles;
-    wide = true;
+    const int items = (s.ql - 1) / tt + 1;
+    if (NT == 1 || s.ql <= tt1) return {tiles, items, false};
     int tile0;  // a last block of one row tile counts once
     const int last = s.ql - (s.ql - 1) / tt * tt;
-    return 2 * tiles - (last <= tt1 ? block_tiles(s.len - s.ql, a.window, s.ql - last, last, tile0) : 0);
+    return {2 * tiles - (last <= tt1 ? block_tiles(s.len - s.ql, a.window, s.ql - last, last, tile0) : 0), items, true};
   });
   int block, unit;
   find_block(run, a, c, tt, tt1, block, unit);
