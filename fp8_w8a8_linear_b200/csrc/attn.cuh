@@ -265,21 +265,36 @@ __global__ void __launch_bounds__(256) attn_join_chunk_kernel(AttnArgs a) {
   const bool live = r < rows;
   const auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? d.y : 2 * (static_cast<int>(blockIdx.x) + i)); };
   float m = -INFINITY, l = 0.0f;
-  for (int i = 0; live && i <= more; ++i) m = fmaxf(m, a.part_ml[slot(i) * ROWS + r].x);
-  const float mb = m == -INFINITY ? 0.0f : m;
   float4 acc[Q];
 #pragma unroll
   for (int q = 0; q < Q; ++q) acc[q] = make_float4(0, 0, 0, 0);
-  for (int i = 0; live && i <= more; ++i) {
-    const float2 ml = a.part_ml[slot(i) * ROWS + r];
-    const float f = ex2(ml.x - mb);
-    l += f * ml.y;
-    if (f == 0.0f) continue;  // a part in which the row saw no key has no o
-    const float4* p = reinterpret_cast<const float4*>(a.part_o) + slot(i) * (D / 4) * ROWS + r;
+  // Two parts at a time, all their loads at once.
+  for (int i = 0; live && i <= more; i += 2) {
+    float2 ml[2];
+    float4 v[2][Q];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const float4 v = p[(warp + 8 * q) * ROWS];
-      acc[q].x += f * v.x, acc[q].y += f * v.y, acc[q].z += f * v.z, acc[q].w += f * v.w;
+    for (int k = 0; k < 2; ++k) {
+      const int64_t at = slot(min(i + k, more));
+      ml[k] = a.part_ml[at * ROWS + r];
+      const float4* p = reinterpret_cast<const float4*>(a.part_o) + at * (D / 4) * ROWS + r;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) v[k][q] = p[(warp + 8 * q) * ROWS];
+    }
+    if (i == more) ml[1] = make_float2(-INFINITY, 0.0f);
+    const float mn = fmaxf(m, fmaxf(ml[0].x, ml[1].x)), mb = mn == -INFINITY ? 0.0f : mn;
+    const float f = ex2(m - mb);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) acc[q].x *= f, acc[q].y *= f, acc[q].z *= f, acc[q].w *= f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float fk = ex2(ml[k].x - mb);
+      l += fk * ml[k].y;
+      if (fk == 0.0f) continue;  // a part in which the row saw no key has no o
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        acc[q].x += fk * v[k][q].x, acc[q].y += fk * v[k][q].y, acc[q].z += fk * v[k][q].z, acc[q].w += fk * v[k][q].w;
     }
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
