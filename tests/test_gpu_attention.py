@@ -113,6 +113,12 @@ def test_rope(lib, T, H, D, R, interleaved, amplitude):
     assert bool((wide[:, 0] == 3.0).all()) and bool((wide[:, H + 1:] == 3.0).all())
 
 
+@pytest.mark.parametrize("T,H,D,R,interleaved", [(1183, 3, 64, 64, False), (5003, 2, 128, 64, True), (2500, 1, 256, 256, False)])
+def test_rope_of_many_tokens(lib, T, H, D, R, interleaved):
+    """Enough tokens for several to a block, the last block short."""
+    test_rope(lib, T, H, D, R, interleaved, 1.0)
+
+
 def test_rope_empty(lib):
     x = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device="cuda")
     assert lib.rope(x, _ints([]), torch.ones(8, device="cuda")).shape == (0, 4, 64)
@@ -150,6 +156,13 @@ def test_kv_append(lib, q_lens, kv_lens, Hq, Hkv, D, page, R, interleaved):
     if Hq:
         assert bool((q_out[n:] == 7.0).all())
     assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv,D,page,R,interleaved", [
+    ([2011, 0, 700, 1, 2402], [2011, 9, 3001, 50, 2500], 6, 2, 64, 16, 64, False), ([1801], [1801], 2, 2, 128, 24, 64, True)])
+def test_kv_append_of_many_tokens(lib, q_lens, kv_lens, Hq, Hkv, D, page, R, interleaved):
+    """Enough tokens for several to a block, sequences starting inside a block's tokens."""
+    test_kv_append(lib, q_lens, kv_lens, Hq, Hkv, D, page, R, interleaved)
 
 
 def test_kv_append_flags_places_that_are_not_there(lib):
@@ -210,6 +223,45 @@ def test_max_q_as_a_bound(lib, max_q):
 def test_long_axis_is_split_and_joined(lib, D, q_len, kv):
     """Few rows over many keys: the keys are shared out over the device."""
     _run(lib, Batch([q_len], [kv], 4, 1, D, 32))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("batch,window", [(33, 0), (97, 50), (450, 0)])
+def test_many_sequences(lib, D, batch, window):
+    """More sequences than the lanes that look for a run, some without new tokens, some without keys."""
+    rng = np.random.default_rng([batch, D])
+    kv = rng.integers(0, 200, batch)
+    _run(lib, Batch([1] * batch, kv.tolist(), 4, 2, D, 16), window=window)
+    q = rng.integers(0, 30, batch)
+    _run(lib, Batch(q.tolist(), (q + kv).tolist(), 4, 2, D, 16), window=window)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv,window", [(12, 4, 0), (4, 4, 0), (16, 2, 700), (5, 1, 129)])
+def test_long_runs_over_items_of_every_kind(lib, D, Hq, Hkv, window):
+    """Runs of many key tiles that pass from items of one row tile to items of two and back, with cuts in both."""
+    q_lens, kv_lens = [300, 20, 1, 70, 513, 129], [5000, 3001, 4100, 900, 2600, 5121]
+    _run(lib, Batch(q_lens, kv_lens, Hq, Hkv, D, 32, extra_rows=1), window=window)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 1], [3000, 40, 700]), ([200, 9, 70], [1500, 2000, 70])])
+def test_two_calls_at_once(lib, q_lens, kv_lens):
+    """Two streams, a workspace each; the calls overlap."""
+    batches = [Batch(q_lens, kv_lens, 8, 2, 128, 16, seed=i) for i in range(2)]
+    args = [(to_dev(B.q), B.dev(), lib.paged_attention_workspace(128)) for B in batches]
+    alone = [lib.paged_attention(q, **c, max_q=max(q_lens), ws=ws) for q, c, ws in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    outs = [[], []]
+    for _ in range(20):
+        for i, (q, c, ws) in enumerate(args):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(lib.paged_attention(q, **c, max_q=max(q_lens), ws=ws))
+    torch.cuda.synchronize()
+    for i, B in enumerate(batches):
+        B.check(alone[i], B.ref())
+        assert all(torch.equal(alone[i], o) for o in outs[i])
+    assert lib.device_status() == 0
 
 
 def test_peaked_scores_and_scales(lib):
