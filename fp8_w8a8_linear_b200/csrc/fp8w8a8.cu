@@ -1487,11 +1487,22 @@ fp8_status rope_checked(const float* inv_freq, int64_t head_dim, int64_t rotary_
   return FP8_OK;
 }
 
-// Tokens per block of the rope kernels: several, so that a block's offsets,
-// pages and angles are worked out together, but one while that would leave
-// fewer than four blocks per SM (a decode step is bound by latency).
-int rope_tokens(const DeviceInfo& dev, int64_t T) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeTokens, T / (4 * dev.sm_count))));
+// Tokens and threads per block of the rope kernels: several tokens, so that a
+// block's offsets, pages and angles are worked out together, but one while
+// that would leave fewer than four blocks per SM (a decode step is bound by
+// latency: there 256 threads, for their shorter loop - 64 tokens of 48 rows
+// 3.4 us, against 3.6 with 128). With several tokens 128 threads, so that more
+// blocks, each in another of its phases, share an SM (8191 tokens of 32 heads
+// 22.5 us, against 24.9 with 256 and 36.6 with 64; up to 4 tokens, against 23.0
+// with 8 and 32.0 with 16), unless a head takes more threads.
+struct RopeBlocks {
+  int tokens;
+  dim3 grid, threads;
+};
+RopeBlocks rope_blocks(const DeviceInfo& dev, int64_t T, int64_t D) {
+  const int tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeTokens, T / (4 * dev.sm_count))));
+  return {tokens, dim3(static_cast<unsigned>((T + tokens - 1) / tokens)),
+          dim3(tokens > 1 && rope_units(static_cast<int>(D)) <= 128 ? 128 : kRopeThreads)};
 }
 
 // A [T, heads, D] bf16 operand with token pitch ld.
@@ -1517,10 +1528,10 @@ extern "C" fp8_status bf16_rope(const uint16_t* x, int64_t ldx, const int32_t* p
   if (!aligned4(positions)) return FP8_ERR_ALIGNMENT;
   DeviceInfo* dev;
   if (fp8_status st = device_info(&dev)) return st;
-  const int tokens = rope_tokens(*dev, T);
-  return launch_pdl_smem(rope_kernel, dim3(static_cast<unsigned>((T + tokens - 1) / tokens)), dim3(kRopeThreads),
-                         static_cast<size_t>(tokens) * r.R * 4, as_stream(stream), x, ldx, positions,
-                         static_cast<int>(T), tokens, static_cast<int>(heads), static_cast<int>(head_dim), r, y, ldy);
+  const RopeBlocks b = rope_blocks(*dev, T, head_dim);
+  return launch_pdl_smem(rope_kernel, b.grid, b.threads, static_cast<size_t>(b.tokens) * r.R * 4, as_stream(stream), x,
+                         ldx, positions, static_cast<int>(T), b.tokens, static_cast<int>(heads),
+                         static_cast<int>(head_dim), r, y, ldy);
 }
 
 extern "C" fp8_status bf16_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
@@ -1546,10 +1557,9 @@ extern "C" fp8_status bf16_kv_append(const uint16_t* k, int64_t ldk, const uint1
   if (fp8_status st = device_info(&dev)) return st;
   const AppendArgs a = {k, v, q, q_out, ldk, ldv, ldq, ldq_out, q ? static_cast<int>(q_heads) : 0,
                         static_cast<int>(T)};
-  const int tokens = rope_tokens(*dev, T);
-  return launch_pdl_smem(kv_append_kernel, dim3(static_cast<unsigned>((T + tokens - 1) / tokens)),
-                         dim3(kRopeThreads), static_cast<size_t>(tokens) * r.R * 4, as_stream(stream), a, c,
-                         tokens, r);
+  const RopeBlocks b = rope_blocks(*dev, T, kv->head_dim);
+  return launch_pdl_smem(kv_append_kernel, b.grid, b.threads, static_cast<size_t>(b.tokens) * r.R * 4,
+                         as_stream(stream), a, c, b.tokens, r);
 }
 
 namespace {

@@ -17,7 +17,7 @@
 
 namespace fp8k {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;  // of a block, at most
 constexpr int kRopeMaxRotary = 512;
 
 struct RopeArgs {
@@ -132,7 +132,7 @@ __device__ __forceinline__ void rope_unit_store(RopeUnit& u, uint16_t* head, con
 // are worked out once, under the first rows' loads. Bound by the bytes (one read,
 // one write).
 constexpr int kRopeFlight = 2;
-constexpr int kRopeTokens = 8;  // a block's, at most
+constexpr int kRopeTokens = 4;  // a block's, at most
 
 struct RopeRow {
   int tok, row;  // row of the token
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const uint16_t* x, i
   pdl_launch_dependents();
   pdl_wait();
   const int t0 = blockIdx.x * tokens, nt = min(tokens, T - t0);
-  const int units = rope_units(D), groups = kRopeThreads / units, group = threadIdx.x / units;
+  const int units = rope_units(D), groups = blockDim.x / units, group = threadIdx.x / units;
   const int unit = threadIdx.x - group * units;
   RopeRow w(group, groups, H);
   if (group >= groups) w.tok = nt;  // a thread left over
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const uint16_t* x, i
       }
     }
     if (first) {
-      for (int k = 0; k < nt; ++k) rope_angles(r, positions[t0 + k], rope_cs + k * (r.R / 2), threadIdx.x, kRopeThreads);
+      for (int k = 0; k < nt; ++k) rope_angles(r, positions[t0 + k], rope_cs + k * (r.R / 2), threadIdx.x, blockDim.x);
       __syncthreads();
       first = false;
     }
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(AppendArgs a, P
   pdl_wait();
   const int t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0);
   int b0 = 0;
-  for (int i0 = 0; i0 < c.batch; i0 += kRopeThreads) {
+  for (int i0 = 0; i0 < c.batch; i0 += blockDim.x) {
     const int i = i0 + threadIdx.x;
     b0 += __syncthreads_count(i < c.batch && c.cu_q[min(i, c.batch - 1) + 1] <= t0);
   }
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(AppendArgs a, P
     where[threadIdx.x] = p;
   }
   // a token's rows: its keys, its queries, its values
-  const int units = rope_units(c.D), groups = kRopeThreads / units, group = threadIdx.x / units;
+  const int units = rope_units(c.D), groups = blockDim.x / units, group = threadIdx.x / units;
   const int unit = threadIdx.x - group * units, nk = c.heads, nkq = c.heads + a.Hq;
   RopeRow w(group, groups, nkq + c.heads);
   if (group >= groups) w.tok = nt;  // a thread left over
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(AppendArgs a, P
     }
     if (first) {
       __syncthreads();  // place, where
-      for (int k = 0; k < nt; ++k) rope_angles(r, where[k], rope_cs + k * (r.R / 2), threadIdx.x, kRopeThreads);
+      for (int k = 0; k < nt; ++k) rope_angles(r, where[k], rope_cs + k * (r.R / 2), threadIdx.x, blockDim.x);
       __syncthreads();
       first = false;
     }

@@ -113,7 +113,7 @@ def test_rope(lib, T, H, D, R, interleaved, amplitude):
     assert bool((wide[:, 0] == 3.0).all()) and bool((wide[:, H + 1:] == 3.0).all())
 
 
-@pytest.mark.parametrize("T,H,D,R,interleaved", [(1183, 3, 64, 64, False), (5003, 2, 128, 64, True), (2500, 1, 256, 256, False)])
+@pytest.mark.parametrize("T,H,D,R,interleaved", [(1183, 3, 64, 64, False), (5003, 2, 128, 64, True), (2500, 1, 256, 256, False), (1190, 1, 2056, 512, True), (1, 1, 4096, 0, False)])
 def test_rope_of_many_tokens(lib, T, H, D, R, interleaved):
     """Enough tokens for several to a block, the last block short."""
     test_rope(lib, T, H, D, R, interleaved, 1.0)
