@@ -720,7 +720,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Attention of the new tokens' q bf16 [T, q_heads, head_dim] over the paged cache (see kv_append), causal, over the
     last ``window`` keys when window > 0; scale defaults to head_dim^-0.5. max_q: no sequence has more new tokens
     (None: T). lse fp32 [T, q_heads] receives ln sum exp of the scores when given. Returns out bf16 [T, q_heads,
-    head_dim]; rows behind cu_q[batch] stay as they are."""
+    head_dim], which must not overlap q; rows behind cu_q[batch] stay as they are."""
     dev, stream = _current(q, "q")
     shape = q.shape
     ldq = _pitch(q, shape, "q")

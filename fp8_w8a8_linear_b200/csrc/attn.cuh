@@ -12,13 +12,20 @@
 // Work. The query heads that share a key/value head are taken together: row
 // r of an item is new token r / G, head r % G of the group, so keys and
 // values are read once for the group. The items' key tiles, laid end to end
-// (sequence, head, tile), are cut into equal runs, one per CTA: a ragged
-// batch, a single long context and a full batch all load the device evenly.
-// An item cut between CTAs leaves an unnormalised o with its maximum and sum
-// for each part in the workspace, and attn_join_kernel adds the parts in
-// order. The cut depends on the lengths and the grid alone, so results are
-// bit-reproducible. Every CTA finds its run by itself from the lengths (a
-// scan over the batch), so a captured graph follows lengths that change.
+// (sequence, head, block of tokens, tile), are cut into equal runs, one per
+// CTA: a ragged batch, a single long context and a full batch all load the
+// device evenly. An item cut between CTAs leaves an unnormalised o with its
+// maximum and sum for each part in the workspace, and a join kernel adds the
+// parts in order. The cut depends on the lengths and the grid alone, so
+// results are bit-reproducible. Every warp finds its CTA's run by itself from
+// the lengths, so a captured graph follows lengths that change.
+//
+// Two kernels: attn_rows_kernel for items of at most 16 rows (max_q * G <= 16,
+// one mma.sync row tile), attn_chunk_kernel for more, on tcgen05. The first is
+// the one whose items cost little: 64 requests of one token (G = 4) over up to
+// 300 keys 21.5 us, with the second 50.2; over up to 8K keys, where both are
+// bound by the cache's bytes, 212 and 216 us; 24 requests of 4 tokens (16 rows)
+// 56.8 and 54.4.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -90,7 +97,10 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
 
-constexpr int kExtraRun = 8;  // units of a run from which on items count their own cost
+// Units of a run from which on items count their own cost (14: a draft check
+// 37.6 us without, 36.5 with); below, a run is about as short as the cost, and
+// whole tiles decide.
+constexpr int kExtraRun = 8;
 
 // A head's key tiles, in units, and its items.
 struct HeadUnits {
@@ -101,10 +111,9 @@ struct HeadUnits {
 
 // Finds CTA `cta`'s run of `ctas`; whole warps call it, each for itself (that
 // needs no barrier: for up to 32 sequences one round of loads and a scan).
-// per_head(b): one of sequence b's heads. Items count `extra` units more
-// where the runs are long enough for that to be the smaller error; a run is
-// never shorter than the distance of two tiles' starts, so that every run
-// inside an item holds a tile of it.
+// per_head(b): one of sequence b's heads. A run is never shorter than the
+// distance of two tiles' starts, so that every run inside an item holds a tile
+// of it.
 template <typename PerHead>
 __device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int ctas, int extra, PerHead per_head) {
   const int lane = lane_id();
@@ -323,7 +332,10 @@ __global__ void __launch_bounds__(256) attn_join_chunk_kernel(AttnArgs a) {
 // ring of shared-memory slots by TMA (one box per page piece); each of four
 // warps takes 16 keys of every tile, with a maximum, sum and o of its own, so
 // the main loop has no exchange between warps; they join through shared
-// memory at an item's end.
+// memory at an item's end. 64 requests of up to 8K keys (8 key/value heads of
+// 128) take 212 us, 6.1 TB/s, 0.95 of the copy rate; one request's 120K keys (4
+// of 256) 87 us, 5.7 TB/s; one of 1000 keys 8.4 us, which is latency: two
+// launches, a look at the lengths, two tiles and the join.
 constexpr int kRowsBN = 64;
 constexpr int kRowsThreads = 160;
 
@@ -704,15 +716,25 @@ __global__ void __launch_bounds__(kRowsThreads)
 //                    operand, O in TMEM.
 // Warps: four per row tile for the softmax, one that issues the MMAs, two that
 // load (queries and keys; values). The softmax of 128 keys and the round trip
-// P -> O += P V -> next S are about as long (some 1700 and 1400 cycles), so
-// two are kept going: head_dim <= 128 with two row tiles in turn, head_dim 256
-// (whose O takes half of TMEM) with two buffers for S of its one row tile, the
-// next scores being formed under this softmax. P is handed over in two halves,
-// so that the product starts under the second half's exponentials.
+// P -> O += P V -> next S -> softmax are about as long (some 1700 and 1950
+// cycles), so two are kept going: head_dim <= 128 with two row tiles, or, where
+// an item has only one, with its key tiles in turn (each group of softmax
+// warps with an o of its own, joined at the end: a draft check 42.5 -> 37.6
+// us); head_dim 256 (whose O takes half of TMEM) with two buffers for S of its
+// one row tile, the next scores being formed under this softmax. P is handed
+// over in two halves, so that the product starts under the second half's
+// exponentials.
 // O is rescaled only when a row's maximum has grown by more than 2^8 since
 // the last time (the factor cancels in the end, and 2^8 times a probability is
 // as exact in bf16 and far from overflow in the sums): after the first tiles
 // hardly ever, so the softmax threads do it themselves.
+// Bound: 8192 tokens of 32 heads (head_dim 128, 8 key/value heads) take 495 us,
+// 1.11 PFLOP/s, at the power limit. Per key tile of two row tiles that is some
+// 3500 cycles, of which the tensor core works 2048 and the exponentials (4 a
+// cycle and scheduler) 2048: what is left is the chain above, which with the
+// two row tiles that TMEM holds (S, P and O of a third do not fit) is not quite
+// covered. Slower: S and P apart in units of 64 keys (583 against 530 us),
+// two threads per row (562), an issuing warp per row tile (613).
 constexpr int kChunkBN = 128;  // keys of a loaded tile
 
 template <int D>
@@ -793,8 +815,12 @@ __device__ __forceinline__ long long chunk_tiles(int first, int len, int window,
   return s;
 }
 
-// Units that a key tile of ntok tokens' rows counts for: two row tiles cost
-// about twice what one does.
+// Units that a key tile of ntok tokens' rows counts for: CTAs' times in a
+// mixed batch fit 1.1 us per key tile of one row tile, 1.9 us of two, and 3.4 us
+// an item (ChunkCfg::kItemUnits; head_dim 256: 2.2 and 3.9 us). A chunk beside
+// decoding requests took 127 us with all tiles alike and takes 110; an 8K
+// prompt, whose early blocks are short items, 547 us without the items' cost
+// and 495 with it.
 __device__ __forceinline__ int tile_units(int ntok, int tt1) { return ntok > tt1 ? 2 : 1; }
 
 // The block of tt tokens at which a run starts in its head, and how far into

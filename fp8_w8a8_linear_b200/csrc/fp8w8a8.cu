@@ -1664,7 +1664,7 @@ extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64
                                            float* lse, void* ws, size_t ws_bytes, void* stream) {
   PagedArgs c;
   if (fp8_status st = paged_checked(kv, T, &c)) return st;
-  if (q_heads < 1 || window < 0 || !(scale > 0.0f) || !(scale <= 3.4e38f)) return FP8_ERR_INVALID_ARG;
+  if (q_heads < 1 || window < 0 || !(scale > 0.0f) || !(scale <= 0x1p126f)) return FP8_ERR_INVALID_ARG;
   if (attn_width(c.D) < 0 || c.page_size % 8 != 0 || q_heads % c.heads != 0 ||
       q_heads / c.heads > 128)
     return FP8_ERR_SHAPE;
@@ -1672,6 +1672,7 @@ extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64
   if (fp8_status st = rows_checked(q, ldq, q_heads, c.D)) return st;
   if (fp8_status st = rows_checked(o, ldo, q_heads, c.D)) return st;
   if (!aligned4(lse) || !aligned16(ws)) return FP8_ERR_ALIGNMENT;
+  if (q == o) return FP8_ERR_INVALID_ARG;
   DeviceInfo* dev;
   if (fp8_status st = device_info(&dev)) return st;
   const AttnWs need = attn_ws(*dev, c.D);

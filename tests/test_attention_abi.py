@@ -85,6 +85,8 @@ def test_paged_attention_refusals(raw):
     assert go(ldq=248) == go(ldo=248) == INVALID
     assert go(q=FAKE + 8) == go(ldo=260) == go(lse=FAKE + 2) == go(ws=FAKE + 8) == ALIGNMENT
     assert go(kv=_kv(cu_q=0)) == INVALID and go(kv=_kv(k=FAKE + 4)) == ALIGNMENT
+    assert go() == INVALID                                         # o is q
+    assert go(o=FAKE + (1 << 20), scale=2.0 ** 127) == INVALID     # times log2 e: past fp32
 
 
 def test_workspace_bytes_of_a_refused_width(raw):
