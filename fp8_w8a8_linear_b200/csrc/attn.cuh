@@ -97,6 +97,34 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return (a | b) >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
 
+// Sum, and sum of the lanes up to one's own, over a warp of numbers that nearly
+// always fit 32 bits together.
+__device__ __forceinline__ long long warp_sum(long long v) {
+  if (!__any_sync(0xFFFFFFFFu, v >> 26)) return __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(v));
+#pragma unroll 1
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+__device__ __forceinline__ long long warp_scan(long long v) {
+  if (!__any_sync(0xFFFFFFFFu, v >> 26)) return warp_scan(static_cast<uint32_t>(v));
+  const int lane = lane_id();
+#pragma unroll 1
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
 // Units of a run from which on items count their own cost (14: a draft check
 // 37.6 us without, 36.5 with); below, a run is about as short as the cost, and
 // whole tiles decide.
@@ -111,26 +139,21 @@ struct HeadUnits {
 
 // Finds CTA `cta`'s run of `ctas`; whole warps call it, each for itself (that
 // needs no barrier: for up to 32 sequences one round of loads and a scan).
-// per_head(b): one of sequence b's heads. A run is never shorter than the
-// distance of two tiles' starts, so that every run inside an item holds a tile
-// of it.
+// per_head(b), called by whole warps: one of sequence b's heads; none for b >=
+// batch. A run is never shorter than the distance of two tiles' starts, so
+// that every run inside an item holds a tile of it.
 template <typename PerHead>
 __device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int ctas, int extra, PerHead per_head) {
   const int lane = lane_id();
-  HeadUnits first = {0, 0, false};
-  if (lane < batch) first = per_head(lane);
-  long long sum = first.units, items = first.items;
-  bool wide = first.wide;
-  for (int b = lane + 32; b < batch; b += 32) {
-    const HeadUnits u = per_head(b);
-    sum += u.units, items += u.items, wide |= u.wide;
+  HeadUnits u = per_head(lane);
+  long long sum = u.units, items = u.items;
+  bool wide = u.wide;
+#pragma unroll 1
+  for (int b0 = 32; b0 < batch; b0 += 32) {
+    const HeadUnits v = per_head(b0 + lane);
+    sum += v.units, items += v.items, wide |= v.wide;
   }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    items += __shfl_xor_sync(0xFFFFFFFFu, items, d);
-  }
-  sum *= heads, items *= heads;
+  sum = warp_sum(sum) * heads, items = warp_sum(items) * heads;
   if (sum < static_cast<long long>(kExtraRun) * ctas) extra = 0;
   sum += items * extra;
   AttnRun r;
@@ -139,20 +162,12 @@ __device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int c
   r.per = static_cast<int>(per);
   if (start >= sum) return r;
   long long base = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < batch; b0 += 32) {
-    if (b0 > 0) {
-      first = {0, 0, false};
-      if (b0 + lane < batch) first = per_head(b0 + lane);
-    }
-    const long long units = first.units + static_cast<long long>(first.items) * extra, mine = units * heads;
-    long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += v;
-    }
-    const long long lo = base + incl - mine;
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, lo <= start && start < lo + mine);
+    if (b0 > 0) u = per_head(b0 + lane);
+    const long long units = u.units + static_cast<long long>(u.items) * extra, incl = warp_scan(units);
+    const long long lo = base + (incl - units) * heads;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, lo <= start && start < lo + units * heads);
     if (hit) {
       const int src = __ffs(hit) - 1;
       const long long off = start - __shfl_sync(0xFFFFFFFFu, lo, src), n = __shfl_sync(0xFFFFFFFFu, units, src);
@@ -162,7 +177,7 @@ __device__ __forceinline__ AttnRun find_run(int batch, int heads, int cta, int c
       r.off = off - r.head * n;
       return r;
     }
-    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    base += __shfl_sync(0xFFFFFFFFu, incl, 31) * heads;
   }
   return r;
 }
@@ -443,6 +458,7 @@ __global__ void __launch_bounds__(kRowsThreads)
   pdl_wait();
   const int cta = blockIdx.x;
   const AttnRun run = find_run(c.batch, c.heads, cta, gridDim.x, 0, [&](int b) -> HeadUnits {
+    if (b >= c.batch) return {0, 0, false};
     const SeqSpan s = seq_span(a, c, b, kRowsBN);
     if (!s.ok && cta == 0) report(FP8_DEV_BAD_INDEX);
     return {s.tiles, 0, false};
@@ -756,26 +772,6 @@ struct ChunkCfg {
                                   (kThreads / 32) * kWalkInts * 4 + (kNT == 2 ? 128 * 8 : 0);
 };
 
-// sum_{i < n} floor((a i + b) / m) for a n + b < 2^32 (the Euclid-like
-// recursion on lattice points under a line).
-__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-  long long s = 0;
-  while (n > 0) {
-    const uint32_t qa = a / m, qb = b / m;
-    s += static_cast<long long>(n) * (n - 1) / 2 * qa + static_cast<long long>(n) * qb;
-    a -= qa * m;
-    b -= qb * m;
-    const uint32_t y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y - n * m;
-    const uint32_t t = m;
-    m = a;
-    a = t;
-  }
-  return s;
-}
-
 // Key tiles that block j (tt tokens from tok0 on, the first at position
 // first + tok0) of a sequence sees: from max(0, p - window + 1) to its last
 // token, in tiles of 128; one where it sees none.
@@ -783,36 +779,6 @@ __device__ __forceinline__ int block_tiles(int first, int window, int tok0, int 
   const int p0 = first + tok0;
   tile0 = max(0, p0 < window ? 0 : p0 - window + 1) / kChunkBN;
   return max(1, (max(0, p0 + ntok) + kChunkBN - 1) / kChunkBN - tile0);
-}
-
-// sum_{i < n} floor((tt i + b) / 128), by shifts when tt is a power of two.
-__device__ __forceinline__ long long tile_sum(int n, int tt, int b) {
-  if (n <= 0) return 0;
-  if (tt & (tt - 1)) return floor_sum(n, kChunkBN, tt, b);
-  const long long nn = n;
-  if (tt >= kChunkBN) return nn * (nn - 1) / 2 * (tt / kChunkBN) + nn * (b / kChunkBN);
-  const int e = __ffs(tt) - 1, k = 7 - e;  // floor((i + c) / 2^k), c = floor(b / tt)
-  const auto below = [&](long long x) {    // sum_{i < x} floor(i / 2^k)
-    const long long q = x >> k;
-    return (q * (q - 1) / 2 << k) + q * (x - (q << k));
-  };
-  const long long cc = b >> e;
-  return below(nn + cc) - below(cc);
-}
-
-// The sum of block_tiles over a sequence's blocks of tt tokens.
-__device__ __forceinline__ long long chunk_tiles(int first, int len, int window, int tt, int ql) {
-  int tile0;
-  if (ql <= tt) return block_tiles(first, window, 0, ql, tile0);
-  const int nb = (ql + tt - 1) / tt;
-  if (len == 0) return nb;
-  const int je = first < 0 ? -first / tt : 0;  // blocks before position 0, one tile each
-  long long s = je + (len + kChunkBN - 1) / kChunkBN +
-                tile_sum(nb - 1 - je, tt, first + (je + 1) * tt + kChunkBN - 1);
-  const int x = first >= window ? -1 : window - 1 - first;
-  const int jw = max(je, x < 0 ? 0 : x / tt + 1);  // first block that starts past tile 0's first key
-  if (nb > jw) s -= tile_sum(nb - jw, tt, first + jw * tt - window + 1);
-  return s;
 }
 
 // Units that a key tile of ntok tokens' rows counts for: CTAs' times in a
@@ -823,8 +789,38 @@ __device__ __forceinline__ long long chunk_tiles(int first, int len, int window,
 // and 495 with it.
 __device__ __forceinline__ int tile_units(int ntok, int tt1) { return ntok > tt1 ? 2 : 1; }
 
+// Block j's units in a head of ql new tokens; none behind the last.
+__device__ __forceinline__ int block_units(const AttnArgs& a, int first, int ql, int j, int tt, int tt1) {
+  const int tok0 = j * tt, ntok = min(tt, ql - tok0);
+  int tile0;
+  return ntok > 0 ? block_tiles(first, a.window, tok0, ntok, tile0) * tile_units(ntok, tt1) : 0;
+}
+
+// find_run's per_head: a lane per sequence of one block; the blocks of longer
+// ones are added up by the whole warp, a block per lane.
+__device__ __forceinline__ HeadUnits chunk_heads(const AttnArgs& a, const PagedArgs& c, int b, int tt, int tt1) {
+  int first = 0, ql = 0;
+  if (b < c.batch) {
+    const SeqSpan s = seq_span(a, c, b, kChunkBN);
+    if (!s.ok && blockIdx.x == 0) report(FP8_DEV_BAD_INDEX);
+    first = s.len - s.ql, ql = s.ql;
+  }
+  HeadUnits u = {0, (ql + tt - 1) / tt, ql > tt1 && tt > tt1};
+  if (ql <= tt) u.units = block_units(a, first, ql, 0, tt, tt1);
+  for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, ql > tt); rest; rest &= rest - 1) {
+    const int src = __ffs(rest) - 1;
+    const int f = __shfl_sync(0xFFFFFFFFu, first, src), q = __shfl_sync(0xFFFFFFFFu, ql, src);
+    long long sum = 0;
+#pragma unroll 1
+    for (int j0 = 0; j0 * tt < q; j0 += 32)
+      sum += __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(block_units(a, f, q, j0 + lane_id(), tt, tt1)));
+    if (lane_id() == src) u.units = sum;
+  }
+  return u;
+}
+
 // The block of tt tokens at which a run starts in its head, and how far into
-// it: the blocks' units are added up, a block per lane (whole warps).
+// it (whole warps).
 __device__ __forceinline__ void find_block(const AttnRun& r, const AttnArgs& a, const PagedArgs& c, int tt, int tt1,
                                            int& block, int& unit) {
   block = unit = 0;
@@ -833,17 +829,10 @@ __device__ __forceinline__ void find_block(const AttnRun& r, const AttnArgs& a, 
   const SeqSpan s = seq_span(a, c, r.seq, kChunkBN);
   const int first = s.len - s.ql;
   long long base = 0;
+#pragma unroll 1
   for (int j0 = 0; j0 * tt < s.ql; j0 += 32) {
-    const int tok0 = (j0 + lane) * tt;
-    int tile0;
-    const int ntok = min(tt, s.ql - tok0);
-    const int mine = ntok > 0 ? block_tiles(first, a.window, tok0, ntok, tile0) * tile_units(ntok, tt1) + r.extra : 0;
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += v;
-    }
+    const uint32_t units = block_units(a, first, s.ql, j0 + lane, tt, tt1);
+    const uint32_t mine = units ? units + r.extra : 0, incl = warp_scan(mine);
     const long long lo = base + incl - mine;
     const uint32_t hit = __ballot_sync(0xFFFFFFFFu, lo <= r.off && r.off < lo + mine);
     if (hit) {
@@ -1493,17 +1482,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   pdl_launch_dependents();  // this CTA holds its TMEM
   pdl_wait();
   const int tt1 = 128 / a.G, tt = NT * tt1;
-  const AttnRun run = find_run(c.batch, c.heads, blockIdx.x, gridDim.x, C::kItemUnits, [&](int b) -> HeadUnits {
-    const SeqSpan s = seq_span(a, c, b, kChunkBN);
-    if (!s.ok && blockIdx.x == 0) report(FP8_DEV_BAD_INDEX);
-    if (s.ql == 0) return {0, 0, false};
-    const long long tiles = chunk_tiles(s.len - s.ql, s.len, a.window, tt, s.ql);
-    const int items = (s.ql - 1) / tt + 1;
-    if (NT == 1 || s.ql <= tt1) return {tiles, items, false};
-    int tile0;  // a last block of one row tile counts once
-    const int last = s.ql - (s.ql - 1) / tt * tt;
-    return {2 * tiles - (last <= tt1 ? block_tiles(s.len - s.ql, a.window, s.ql - last, last, tile0) : 0), items, true};
-  });
+  const AttnRun run = find_run(c.batch, c.heads, blockIdx.x, gridDim.x, C::kItemUnits,
+                               [&](int b) { return chunk_heads(a, c, b, tt, tt1); });
   int block, unit;
   find_block(run, a, c, tt, tt1, block, unit);
   w.start(a, c, run, block, unit, tt, tt1);

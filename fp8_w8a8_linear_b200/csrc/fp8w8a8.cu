@@ -1646,7 +1646,9 @@ fp8_status launch_attn_chunk(const DeviceInfo& dev, AttnArgs a, const PagedArgs&
   if (fp8_status st = launch_pdl_smem(attn_chunk_kernel<D>, dim3(dev.sm_count), dim3(C::kThreads), C::kSmem,
                                       stream, tmQ, tmK, tmV, a, c))
     return st;
-  return launch_pdl(attn_join_chunk_kernel<D, C::kRows>, dim3(dev.sm_count, C::kRows / 32), dim3(256), stream, a);
+  const int64_t rows = std::min<int64_t>(C::kRows, static_cast<int64_t>(a.max_q) * a.G);
+  return launch_pdl(attn_join_chunk_kernel<D, C::kRows>, dim3(dev.sm_count, static_cast<unsigned>((rows + 31) / 32)),
+                    dim3(256), stream, a);
 }
 
 }  // namespace
