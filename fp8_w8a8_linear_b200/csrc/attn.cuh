@@ -1178,11 +1178,14 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
     if (join) {
       if (tile == 1) {
         ml[rr] = make_float2(mu, l);
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_full);
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(ml_full + 8, joins & 1, abort_w));  // read
+        tc_fence_after();
       } else {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_ab(ml_full, joins & 1, abort_w));
+        tc_fence_after();
         const float2 x = ml[rr];
         const float mm = fmaxf(mu, x.x), mb = mm == -INFINITY ? 0.0f : mm;
         f0 = ex2(mu - mb);
