@@ -781,6 +781,15 @@ __device__ __forceinline__ int block_tiles(int first, int window, int tok0, int 
   return max(1, (max(0, p0 + ntok) + kChunkBN - 1) / kChunkBN - tile0);
 }
 
+// How a key or value tile lies in shared memory: groups of 64 elements one
+// after the other, each with all rows; or, where pages come in pieces of eight
+// rows, the groups of a piece side by side, so that one box brings the piece
+// whole: half as many boxes at head_dim 128, of which a warp starts one in some
+// 60 cycles (pages of 8: a chunk beside decoding requests 147 -> 109 us). Longer
+// pieces cannot lie like that: their rows' distances would not be even.
+// (Both ways in one kernel cost the issuing thread 4 % of a prompt.)
+constexpr int kPackedRows = 8;
+
 // Units that a key tile of ntok tokens' rows counts for: CTAs' times in a
 // mixed batch fit 1.1 us per key tile of one row tile, 1.9 us of two, and 3.4 us
 // an item (ChunkCfg::kItemUnits; head_dim 256: 2.2 and 3.9 us). A chunk beside
@@ -957,18 +966,18 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Shared-memory descriptors by halves: the upper one is the same for all
-// operands here (1024 bytes from eight rows, or eight of K, to the next;
-// version 1; 128-byte swizzle), the lower one is the address in 16-byte
-// units, to which offsets are simply added, and the lead offset: unused
-// where K is contiguous, and where M/N is (the values: 64 elements of N by
-// eight keys make a 1024-byte atom) the bytes from one group of 64 to the next.
+// Shared-memory descriptors by halves: the upper one has the bytes from eight
+// rows (or eight of K) to the next, 1024 unless said, version 1 and the
+// 128-byte swizzle, the lower one the address in 16-byte units, to which
+// offsets are simply added, and the lead offset: unused where K is contiguous,
+// and where M/N is (the values: 64 elements of N by eight keys make a
+// 1024-byte atom) the bytes from one group of 64 to the next.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t lead_bytes) {
   return (smem_addr >> 4) | (lead_bytes >> 4 << 16);
 }
-__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
-  return (static_cast<uint64_t>(kDescHi) << 32) | lo;
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi = kDescHi) {
+  return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 constexpr uint32_t kIdescBMnMajor = 1u << 16;  // operand B's contiguous dimension is N
 
@@ -1285,7 +1294,7 @@ struct ChunkBars {
 // The MMAs, issued by one thread. It shares its scheduler and instruction
 // cache with two softmax warps, so what it does between two products counts:
 // the slots' waits come before the probabilities' and the releases last.
-template <int D>
+template <int D, bool PACKED>
 __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedArgs& c, ChunkWalk& w, int tt1,
                                                 uint32_t tmem, uint32_t q_smem, uint32_t slot0, uint32_t bars,
                                                 uint32_t abort_w, bool& issued) {
@@ -1294,7 +1303,12 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
   constexpr int NT = C::kNT, NS = C::kSlots, PARTS = C::kParts;
   constexpr uint32_t kIdescS = idesc_kind<kKindBF16>(128, kChunkBN);
   constexpr uint32_t kIdescO = idesc_kind<kKindBF16>(128, D) | kIdescBMnMajor;
-  const uint32_t q_lo = desc_lo(q_smem, 16), k_lo = desc_lo(slot0, 16), v_lo = desc_lo(slot0, C::kVKeys * 128);
+  // keys and values as the loads leave them (see kPackedRows)
+  const uint32_t q_lo = desc_lo(q_smem, 16), k_lo = desc_lo(slot0, 16),
+                 v_lo = desc_lo(slot0, PACKED ? 1024 : C::kVKeys * 128);
+  constexpr uint32_t k_hi = PACKED ? kDescHi + (C::kKCols / 64 - 1) * 64 : kDescHi,
+                     v_hi = PACKED ? kDescHi + (D / 64 - 1) * 64 : kDescHi;
+  constexpr uint32_t k_group = PACKED ? 64 : 1024, v_step = PACKED ? D * 2 : 128;
   int slot = 0;  // next slot in load order
   uint32_t phase = 0, q_par = 0, p_par = 0;
   const auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_ab(bars + bar, parity, abort_w); };
@@ -1324,7 +1338,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
       const int p = k * 16 / C::kKCols, kk = k - p * (C::kKCols / 16);
       umma_kind<kKindBF16>(tmem + b * kChunkBN,
                            desc_of(q_lo + (q_tile * (128 * D * 2) + (k >> 2) * 16384 + (k & 3) * 32) / 16),
-                           desc_of(kb[p] + ((kk >> 2) * 16384 + (kk & 3) * 32) / 16), kIdescS, k > 0);
+                           desc_of(kb[p] + (kk >> 2) * k_group + (kk & 3) * 2, k_hi), kIdescS, k > 0);
     }
     umma_commit(bars + B::kSFull + 8 * b);
     issued = true;
@@ -1343,7 +1357,7 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
 #pragma unroll
       for (int k = 4 * half; k < 4 * half + 4; ++k) {
         const int p = k * 16 / C::kVKeys, kk = k - p * (C::kVKeys / 16);
-        umma_bf16_ts(tmem + 256 + tile * D, tmem + b * kChunkBN + 8 * k, desc_of(vb[p] + kk * 128), kIdescO,
+        umma_bf16_ts(tmem + 256 + tile * D, tmem + b * kChunkBN + 8 * k, desc_of(vb[p] + kk * v_step, v_hi), kIdescO,
                      k > 0 ? 1u : static_cast<uint32_t>(add));
       }
     }
@@ -1417,18 +1431,18 @@ __device__ __forceinline__ bool chunk_issue_all(const AttnArgs& a, const PagedAr
   return true;
 }
 
-template <int D>
+template <int D, bool PACKED>
 __device__ __forceinline__ void chunk_issue(const AttnArgs& a, const PagedArgs& c, ChunkWalk& w, int tt1, uint32_t tmem,
                                             uint32_t q_smem, uint32_t slot0, uint32_t bars, uint32_t abort_w) {
   bool issued = false;
-  if (!chunk_issue_all<D>(a, c, w, tt1, tmem, q_smem, slot0, bars, abort_w, issued) && issued) {
+  if (!chunk_issue_all<D, PACKED>(a, c, w, tt1, tmem, q_smem, slot0, bars, abort_w, issued) && issued) {
     // everything issued is done before TMEM is given back (bounded)
     umma_commit(bars + ChunkBars<D>::kDrained);
     mbar_wait(bars + ChunkBars<D>::kDrained, 0);
   }
 }
 
-template <int D>
+template <int D, bool PACKED>
 __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     attn_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const AttnArgs a, const PagedArgs c) {
@@ -1496,7 +1510,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     chunk_softmax<D>(a, c, w, tile, tt1, tmem, s_full + 8 * tile, p_full + 16 * tile, o_done + 8 * tile,
                      full0 + B::kMlFull, ml, abort_w, run.per);
   } else if (warp == kMmaWarp) {
-    if (lane == 0) chunk_issue<D>(a, c, w, tt1, tmem, q_smem, slot0, full0, abort_w);
+    if (lane == 0) chunk_issue<D, PACKED>(a, c, w, tt1, tmem, q_smem, slot0, full0, abort_w);
   } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
     
     // ------------------------------------------------------------- loads
@@ -1506,9 +1520,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const CUtensorMap* map = keys ? &tmK : &tmV;
     const int rows = a.box_rows;
     constexpr int kColGroups = C::kKCols / 64, kAllGroups = D / 64;
-    const uint32_t box_bytes = static_cast<uint32_t>(rows) * 128;
     // a slot's boxes, one per lane: piece `piece` (rows keys), column group grp
-    const int groups = keys ? kColGroups : kAllGroups;
+    // (packed: all groups)
+    const int all = keys ? kColGroups : kAllGroups, groups = PACKED ? 1 : all;
+    const uint32_t box_bytes = static_cast<uint32_t>(rows) * (PACKED ? all * 128 : 128);
     const int pieces = (keys ? kChunkBN : C::kVKeys) / rows;  // per slot
     const int piece = lane / groups, grp = lane % groups;
     const uint32_t dst0 = slot0 + grp * (pieces * box_bytes) + piece * box_bytes;
@@ -1573,8 +1588,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
           for (int r = 0; r < C::kVKeys; ++r) {
             const int key = p * C::kVKeys + r;
             if ((key < lo || key >= hi) && lane < D / 8)
-              *reinterpret_cast<uint4*>(slots + slot * C::kSlotBytes + (lane >> 3) * (C::kVKeys * 128) + r * 128 +
-                                        (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(slots + slot * C::kSlotBytes + (lane & 7) * 16 +
+                                        (PACKED ? (r >> 3) * (D * 16) + (lane >> 3) * 1024 + (r & 7) * 128
+                                                : (lane >> 3) * (C::kVKeys * 128) + r * 128)) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_shared();
           __syncwarp();

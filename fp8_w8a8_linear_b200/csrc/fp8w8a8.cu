@@ -231,9 +231,10 @@ fp8_status set_attn_attr(int sm_count, int* ctas) {
       n < 1)
     return FP8_ERR_CUDA;
   *ctas = n * sm_count;
-  if (cudaFuncSetAttribute(attn_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(ChunkCfg<D>::kSmem)) != cudaSuccess)
-    return FP8_ERR_CUDA;
+  for (auto kernel : {attn_chunk_kernel<D, false>, attn_chunk_kernel<D, (D > 64)>})
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(ChunkCfg<D>::kSmem)) != cudaSuccess)
+      return FP8_ERR_CUDA;
   return FP8_OK;
 }
 
@@ -1630,6 +1631,7 @@ fp8_status launch_attn_chunk(const DeviceInfo& dev, AttnArgs a, const PagedArgs&
   using C = ChunkCfg<D>;
   a.box_rows = std::min(C::kVKeys, c.page_size & -c.page_size);
   const int tt1 = 128 / a.G;
+  const bool packed = D > 64 && a.box_rows == kPackedRows;
   CUtensorMap tmQ, tmK, tmV;
   EncodeTiledFn fn = encode_fn();
   if (!fn) return FP8_ERR_CUDA;
@@ -1641,10 +1643,12 @@ fp8_status launch_attn_chunk(const DeviceInfo& dev, AttnArgs a, const PagedArgs&
   if (fn(&tmQ, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(a.q), dims, strides, box, estr,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-      !make_tmap_paged(&tmK, c.k, c, a.box_rows, 1, a.q) || !make_tmap_paged(&tmV, c.v, c, a.box_rows, 1, a.q))
+      !make_tmap_paged(&tmK, c.k, c, a.box_rows, packed ? C::kKCols / 64 : 1, a.q) ||
+      !make_tmap_paged(&tmV, c.v, c, a.box_rows, packed ? D / 64 : 1, a.q))
     return FP8_ERR_CUDA;
-  if (fp8_status st = launch_pdl_smem(attn_chunk_kernel<D>, dim3(dev.sm_count), dim3(C::kThreads), C::kSmem,
-                                      stream, tmQ, tmK, tmV, a, c))
+  const auto kernel = packed ? attn_chunk_kernel<D, (D > 64)> : attn_chunk_kernel<D, false>;
+  if (fp8_status st = launch_pdl_smem(kernel, dim3(dev.sm_count), dim3(C::kThreads), C::kSmem, stream, tmQ, tmK,
+                                      tmV, a, c))
     return st;
   const int64_t rows = std::min<int64_t>(C::kRows, static_cast<int64_t>(a.max_q) * a.G);
   return launch_pdl(attn_join_chunk_kernel<D, C::kRows>, dim3(dev.sm_count, static_cast<unsigned>((rows + 31) / 32)),

@@ -306,6 +306,20 @@ def test_nan_where_no_token_looks(lib):
         _run(lib, B, window=window)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page,window", [(8, 0), (8, 90), (24, 100), (40, 1), (16, 130)])
+def test_small_pages_with_nan_around_the_keys(lib, D, page, window):
+    """Chunks whose first and last tiles hold values that must not count, pages in pieces of 8 rows and of 16."""
+    q_lens = [130, 1, 70]
+    B = Batch(q_lens, [900, 411, 70], 6, 2, D, page)
+    for b, n in enumerate(q_lens):
+        first = B.kv_lens[b] - n - window + 1 if window else 0
+        for j in range(first):
+            B.k[B.table[b, j // page], j % page] = NAN_BITS
+            B.v[B.table[b, j // page], j % page] = NAN_BITS
+    _run(lib, B, window=window)
+
+
 def test_offsets_past_32_bits(lib):
     """A cache of 2^31 elements and more, the pages in use at its end."""
     page, Hkv, D = 64, 8, 256
