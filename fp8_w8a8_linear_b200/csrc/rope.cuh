@@ -220,8 +220,9 @@ struct AppendArgs {
 
 // The new tokens' keys (rotated) and values go to their places in the cache,
 // their queries (rotated) to q_out. The sequence of a block's first token is
-// the number of offsets at or below it, counted by the block; those of its
-// other tokens follow from there.
+// the number of offsets at or below it, counted by the block (one look for up
+// to as many sequences as threads, two for their square); those of its other
+// tokens follow from there.
 __global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(AppendArgs a, PagedArgs c, int tokens,
                                                                  RopeArgs r) {
   extern __shared__ __align__(16) float2 rope_cs[];  // [tokens][R / 2]
@@ -231,10 +232,15 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(AppendArgs a, P
   pdl_wait();
   const int t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0);
   int b0 = 0;
-  for (int i0 = 0; i0 < c.batch; i0 += blockDim.x) {
-    const int i = i0 + threadIdx.x;
-    b0 += __syncthreads_count(i < c.batch && c.cu_q[min(i, c.batch - 1) + 1] <= t0);
+  int end = c.batch;  // it is in [b0, end]
+#pragma unroll 1
+  while (end - b0 > static_cast<int>(blockDim.x)) {  // thread i looks past the i-th `step` sequences
+    const int step = (end - b0 + blockDim.x - 1) / blockDim.x, i = b0 + (threadIdx.x + 1) * step;
+    b0 += step * __syncthreads_count(i <= end && c.cu_q[min(i, end)] <= t0);
+    end = min(end, b0 + step);
   }
+  const int next = b0 + threadIdx.x + 1;
+  b0 += __syncthreads_count(next <= end && c.cu_q[min(next, end)] <= t0);
   if (threadIdx.x < nt) {
     const int t = t0 + threadIdx.x;
     int b = b0;

@@ -159,7 +159,8 @@ def test_kv_append(lib, q_lens, kv_lens, Hq, Hkv, D, page, R, interleaved):
 
 
 @pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv,D,page,R,interleaved", [
-    ([2011, 0, 700, 1, 2402], [2011, 9, 3001, 50, 2500], 6, 2, 64, 16, 64, False), ([1801], [1801], 2, 2, 128, 24, 64, True)])
+    ([2011, 0, 700, 1, 2402], [2011, 9, 3001, 50, 2500], 6, 2, 64, 16, 64, False), ([1801], [1801], 2, 2, 128, 24, 64, True),
+    ([1] * 1300, [5] * 1300, 2, 1, 64, 8, 32, False), ([0, 3, 0, 0, 1, 2] * 217, [0, 3, 4, 0, 9, 30] * 217, 1, 1, 64, 8, 64, True)])
 def test_kv_append_of_many_tokens(lib, q_lens, kv_lens, Hq, Hkv, D, page, R, interleaved):
     """Enough tokens for several to a block, sequences starting inside a block's tokens."""
     test_kv_append(lib, q_lens, kv_lens, Hq, Hkv, D, page, R, interleaved)
