@@ -191,6 +191,10 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr int kRowsMax = 16;  // rows of an attn_rows_kernel item
 constexpr float kLn2 = 0.69314718055994531f;
 
+// 1 / l for a sum of probabilities: 0 where no key was seen, so that o is 0;
+// a NaN stays, so that it reaches o even where that was finite.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+
 // ------------------------------------------------------------------ join
 // The parts of one cut item, in order: the first in slot `slot`, then slot
 // 2 (cta + i) of the `more` following CTAs. Rows of the item: token t0 + r /
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(AttnArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += so[i][lane * E + e];
   const int t = d.z + r / a.G, h = d.w + r % a.G;
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = inverse_sum(l);
   uint16_t* o = a.o + t * a.ldo + static_cast<int64_t>(h) * D + lane * (E < 4 ? E : 4);
   if constexpr (E == 2) {
     *reinterpret_cast<uint32_t*>(o) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
@@ -315,13 +319,15 @@ __global__ void __launch_bounds__(256) attn_join_chunk_kernel(AttnArgs a) {
     for (int k = 0; k < 2; ++k) {
       const float fk = ex2(ml[k].x - mb);
       l += fk * ml[k].y;
-      if (fk == 0.0f) continue;  // a part in which the row saw no key has no o
+      // A part in which the row saw no key has no o. The factor does not tell
+      // (maxima pass over NaN, so it may be 0 where l and o hold one).
+      if (ml[k].x == -INFINITY && ml[k].y == 0.0f) continue;
 #pragma unroll
       for (int q = 0; q < Q; ++q)
         acc[q].x += fk * v[k][q].x, acc[q].y += fk * v[k][q].y, acc[q].z += fk * v[k][q].z, acc[q].w += fk * v[k][q].w;
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = inverse_sum(l);
 #pragma unroll
   for (int q = 0; q < Q; ++q)
     *reinterpret_cast<uint2*>(&so[lane][4 * (warp + 8 * q)]) =
@@ -677,7 +683,7 @@ __global__ void __launch_bounds__(kRowsThreads)
     }
     const bool whole = w.t == 0 && n == w.s.tiles;
     const int part = 2 * cta + (first ? 0 : 1);
-    const float inv = jl > 0.0f ? 1.0f / jl : 0.0f;
+    const float inv = inverse_sum(jl);
     const int tok = w.s.q0 + r / a.G, head = h0 + r % a.G;
 #pragma unroll
     for (int cb = 0; cb < D / 32; ++cb) {
@@ -1224,7 +1230,7 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
       }
     };
     if (to > from && !idle && !(turns && tile == 1)) {
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv = inverse_sum(l);
       if (whole) {
         // Four lanes turn their rows' 16-byte pieces among themselves, so that
         // a store covers 8 rows x 64 bytes instead of 32 x 16.

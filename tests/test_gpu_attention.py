@@ -497,3 +497,46 @@ def test_binding_refusals(lib):
     with pytest.raises(ValueError):
         lib.kv_append(q[:, :2], q[:, :2], **c, q_out=q)
     assert lib.device_status() == 0
+
+
+# Whole items and cut ones of both kernels: (q_lens, kv_lens, Hq, Hkv). Many short sequences fill every run with whole items,
+# one long context is cut over the device.
+KINDS = [([1] * 40, [60] * 40, 16, 4), ([1], [20000], 4, 1), ([9] * 40, [60] * 40, 16, 4), ([40], [12345], 4, 1), ([300], [6000], 4, 1)]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("what", ["query", "key", "value"])
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv", KINDS)
+def test_a_nan_that_a_token_sees_reaches_its_output(lib, D, what, q_lens, kv_lens, Hq, Hkv):
+    """A query row, a key or one element of a value is NaN: it reaches the rows that see it, however the work was cut and
+    however little the part with the key weighs in the sum; what does not see it stays as it is (a NaN value may reach its
+    column of the sequence's other rows)."""
+    last = len(q_lens) - 1
+    for scale in (None, 8.0):      # 8: parts' maxima lie hundreds apart
+        B = Batch(q_lens, kv_lens, Hq, Hkv, D, 16)
+        ref = B.ref(scale=scale)
+        j = kv_lens[last] // 3 if q_lens[last] == 1 else kv_lens[last] - q_lens[last] // 2
+        page = B.table[last, j // 16], j % 16, 0
+        nan, free = np.zeros((2, B.T, Hq, D), bool)
+        if what == "query":
+            t, h = int(B.cu_q[last + 1]) - 1, Hq // 2
+            B.q[t, h, 3] = NAN_BITS
+            nan[t, h] = True
+        else:
+            sees = np.zeros((B.T, Hq, 1), bool)
+            sees[:, : Hq // Hkv, 0] = ((B.seq == last) & (B.pos >= j))[:, None]
+            if what == "key":
+                B.k[page][D - 1] = NAN_BITS
+                nan |= sees
+            else:
+                B.v[page][D - 1] = NAN_BITS
+                nan[..., D - 1:] = sees
+                free[B.seq == last, : Hq // Hkv, D - 1] = True
+        assert nan.any()
+        out = lib.paged_attention(to_dev(B.q), **B.dev(), scale=scale, max_q=max(q_lens))
+        got = bf16_values(out)
+        assert np.isnan(got[nan]).all(), (scale, int((~np.isnan(got[nan])).sum()))
+        tol, _ = A.attention_tolerance(ref, D)
+        rest = ~(nan | free)
+        assert np.all(np.abs(got - ref["out"])[rest] <= tol[rest]), scale
+        assert lib.device_status() == 0
