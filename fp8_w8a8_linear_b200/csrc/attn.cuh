@@ -195,6 +195,10 @@ constexpr float kLn2 = 0.69314718055994531f;
 // a NaN stays, so that it reaches o even where that was finite.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
+// lse from a row's maximum and sum (base 2): -inf where no key was seen, and
+// only there.
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
 // ------------------------------------------------------------------ join
 // The parts of one cut item, in order: the first in slot `slot`, then slot
 // 2 (cta + i) of the `more` following CTAs. Rows of the item: token t0 + r /
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(AttnArgs a) {
                      pack_bf16x2(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv));
   }
   if (a.lse && lane == 0)
-    a.lse[static_cast<int64_t>(t) * a.Hq + h] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    a.lse[static_cast<int64_t>(t) * a.Hq + h] = lse_of(m, l);
 }
 
 // Parts of attn_chunk_kernel, [slot][D / 4][row][4]: written by one thread
@@ -333,8 +337,7 @@ __global__ void __launch_bounds__(256) attn_join_chunk_kernel(AttnArgs a) {
     *reinterpret_cast<uint2*>(&so[lane][4 * (warp + 8 * q)]) =
         make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
   if (a.lse && live && warp == 0)
-    a.lse[static_cast<int64_t>(d.z + r / a.G) * a.Hq + d.w + r % a.G] =
-        l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    a.lse[static_cast<int64_t>(d.z + r / a.G) * a.Hq + d.w + r % a.G] = lse_of(m, l);
   __syncthreads();
   for (int i = threadIdx.x; i < 32 * (D / 8); i += 256) {
     const int rr = i / (D / 8), c8 = i % (D / 8), ro = blockIdx.y * 32 + rr;
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(kRowsThreads)
       if (!whole)
         a.part_ml[static_cast<int64_t>(part) * kRowsMax + r] = make_float2(jm, jl);
       else if (a.lse)
-        a.lse[static_cast<int64_t>(tok) * a.Hq + head] = jl > 0.0f ? (jm + log2f(jl)) * kLn2 : -INFINITY;
+        a.lse[static_cast<int64_t>(tok) * a.Hq + head] = lse_of(jm, jl);
     }
     if (w.t == 0 && !whole) {  // the item's first part: what follows joins it
       desc_written = true;
@@ -1276,7 +1279,7 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
       if (!whole)
         a.part_ml[static_cast<int64_t>(part) * C::kRows + row] = make_float2(mu, l);
       else if (a.lse)
-        a.lse[tok * a.Hq + head] = l > 0.0f ? (mu + log2f(l)) * kLn2 : -INFINITY;
+        a.lse[tok * a.Hq + head] = lse_of(mu, l);
     }
     if (w.t == 0 && !whole)
       desc = join_desc(w.more(per, tt1), part, w.q0 + w.tok0, w.h * a.G, w.ntok * a.G);

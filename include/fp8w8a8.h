@@ -632,8 +632,10 @@ size_t bf16_paged_attention_workspace_bytes(int64_t head_dim);
  * 0 only those with j > p - window:
  *   s_j = scale * q . k_j,  o = sum_j softmax(s)_j v_j (bf16),
  *   lse = ln sum_j exp(s_j) (fp32; not computed when NULL).
- * A token that sees no key (q_len > kv_len) gets o = 0 and lse = -inf. The
- * keys are walked once with a running maximum and sum; scores, statistics
+ * A token that sees no key (q_len > kv_len) gets o = 0 and lse = -inf. A token
+ * that sees a NaN score, or one past fp32's largest number (which counts as
+ * +inf), gets NaN in o and lse; scores below its least number weigh nothing.
+ * The keys are walked once with a running maximum and sum; scores, statistics
  * and o in fp32, the probabilities rounded to bf16 for their product with v.
  * The sum order depends on the batch's lengths and the device alone, so
  * results are bit-reproducible. Values behind kv_len, and keys and values

@@ -540,3 +540,30 @@ def test_a_nan_that_a_token_sees_reaches_its_output(lib, D, what, q_lens, kv_len
         rest = ~(nan | free)
         assert np.all(np.abs(got - ref["out"])[rest] <= tol[rest]), scale
         assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv", KINDS)
+def test_lse_of_rows_with_nan_is_not_that_of_rows_without_keys(lib, D, q_lens, kv_lens, Hq, Hkv):
+    """lse is NaN for a NaN query row and for a row whose scores pass fp32 (whose o is NaN too); -inf stays for rows that see no key."""
+    B = Batch(q_lens + [3], kv_lens + [2], Hq, Hkv, D, 16)     # the first of the three sees nothing
+    t = int(B.cu_q[-2]) - 1
+    B.q[t, 1, 5] = NAN_BITS
+    big = t, 2
+    j = B.kv_lens[-2] // 2 if q_lens[-1] == 1 else B.kv_lens[-2] - q_lens[-1] // 2
+    B.q[big] = f32_to_bf16_bits(np.full(D, 2.0 ** 70, np.float32))
+    ref = B.ref()
+    for h in range(Hkv):
+        B.k[B.table[len(q_lens) - 1, j // 16], j % 16, h] = f32_to_bf16_bits(np.full(D, 2.0 ** 70, np.float32))
+    hit = (B.seq == len(q_lens) - 1) & (B.pos >= j)
+    lse = torch.full((B.T, Hq), 7.0, device="cuda")
+    out = lib.paged_attention(to_dev(B.q), **B.dev(), max_q=max(B.q_lens), lse=lse)
+    got, l = bf16_values(out), f32(lse)
+    for row in ((t, 1), big):
+        assert np.isnan(got[row]).all() and np.isnan(l[row]), row
+    assert np.all(np.isneginf(l[B.T - 3])) and np.all(got[B.T - 3] == 0)
+    _, tol = A.attention_tolerance(ref, D)
+    rest = ~hit
+    rest[B.T - 3] = False
+    assert np.all(np.abs(l[rest] - ref["lse"][rest]) <= tol[rest])
+    assert lib.device_status() == 0
