@@ -1189,6 +1189,9 @@ __device__ __forceinline__ void chunk_softmax(const AttnArgs& a, const PagedArgs
       if (!ok) break;
       tc_fence_after();
     }
+    // A finite score that the scale takes past fp32 gives the maximum +inf,
+    // from which the fused product and sum sees it as -inf: the sum says NaN.
+    if (mu == INFINITY) l = __int_as_float(0x7FFFFFFF);
     // Two groups on one row tile: the second leaves its rows' statistics in
     // shared memory, the first reads them and both groups' o (its lanes of
     // TMEM are the same) and goes on alone.

@@ -567,3 +567,18 @@ def test_lse_of_rows_with_nan_is_not_that_of_rows_without_keys(lib, D, q_lens, k
     rest[B.T - 3] = False
     assert np.all(np.abs(l[rest] - ref["lse"][rest]) <= tol[rest])
     assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv", KINDS)
+def test_scores_that_only_their_scale_takes_past_fp32(lib, D, q_lens, kv_lens, Hq, Hkv):
+    """q . k is finite (2^120 D, D = 64 and 128) and scale times it is not: NaN in o and lse, as where q . k is not."""
+    B = Batch(q_lens, kv_lens, Hq, Hkv, D, 16)
+    t, b = B.T - 1, len(q_lens) - 1
+    j = kv_lens[b] // 2 if q_lens[b] == 1 else kv_lens[b] - q_lens[b] // 2
+    B.q[t, 1] = f32_to_bf16_bits(np.full(D, 2.0 ** 60, np.float32))
+    B.k[B.table[b, j // 16], j % 16, 0] = f32_to_bf16_bits(np.full(D, 2.0 ** 60, np.float32))
+    lse = torch.full((B.T, Hq), 7.0, device="cuda")
+    out = lib.paged_attention(to_dev(B.q), **B.dev(), scale=32.0, max_q=max(q_lens), lse=lse)
+    assert np.isnan(bf16_values(out)[t, 1]).all() and np.isnan(f32(lse)[t, 1])
+    assert lib.device_status() == 0
