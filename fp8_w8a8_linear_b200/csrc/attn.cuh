@@ -1447,8 +1447,11 @@ template <int D, bool PACKED>
 __device__ __forceinline__ void chunk_issue(const AttnArgs& a, const PagedArgs& c, ChunkWalk& w, int tt1, uint32_t tmem,
                                             uint32_t q_smem, uint32_t slot0, uint32_t bars, uint32_t abort_w) {
   bool issued = false;
-  if (!chunk_issue_all<D, PACKED>(a, c, w, tt1, tmem, q_smem, slot0, bars, abort_w, issued) && issued) {
-    // everything issued is done before TMEM is given back (bounded)
+  chunk_issue_all<D, PACKED>(a, c, w, tt1, tmem, q_smem, slot0, bars, abort_w, issued);
+  if (issued) {
+    // Everything issued is done before TMEM is given back and the CTA's shared
+    // memory goes (bounded), also where a softmax warp gave up on the last
+    // product. In a sound run the softmax's own end is later.
     umma_commit(bars + ChunkBars<D>::kDrained);
     mbar_wait(bars + ChunkBars<D>::kDrained, 0);
   }
@@ -1477,6 +1480,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   const uint32_t q_smem = smem_u32(smem), slot0 = smem_u32(slots);
   const int warp = warp_id(), lane = lane_id();
   constexpr int kMmaWarp = NT * 4, kLoadWarp = NT * 4 + 1;  // and kLoadWarp + 1
+  // Test hook: CTA 0 skips one slot's load (no arrive, no copies).
+  const int drop = blockIdx.x == 0 && warp >= kLoadWarp ? *const_cast<volatile int*>(&g_fault_drop_step) : -1;
 
   if (threadIdx.x == 0) {
     st_shared_volatile_u32(abort_w, 0u);
@@ -1586,6 +1591,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
         const bool mine = has_box && page >= 0;
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes;
         if (filled >= NS && !wait(empty0 + 8 * slot, phase ^ 1)) return;
+        if (filled == drop) {
+          pass();
+          continue;
+        }
         const uint32_t bar = edge ? v_tmp : full0 + 8 * slot;
         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         __syncwarp();

@@ -47,3 +47,30 @@ def test_a_dropped_stage_times_out_and_the_device_stays_usable(lib, M, N, K, ste
     ok, worst = oracle.check_linear(bf16_values(y), y_ref, abs_s)
     assert ok, worst
     assert lib.device_status() == 0
+
+
+# The attention of chunks: two row tiles, both kinds of item, one row tile (whose key tiles two groups take in turn), and
+# items of one key tile. At head_dim 256 a tile has two loads, otherwise one.
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens,steps", [
+    ([300], [6000], (0, 1, 7)), ([40, 9], [20000, 700], (2, 5)), ([9], [40000], (0, 1, 2, 7)), ([70], [70], (0, 1))])
+def test_a_dropped_load_of_a_chunk_times_out_and_the_device_stays_usable(lib, D, q_lens, kv_lens, steps):
+    from tests.test_gpu_attention import Batch
+
+    B = Batch(q_lens, kv_lens, 16, 4, D, 32)
+    q, c, ws = to_dev(B.q), B.dev(), lib.paged_attention_workspace(D)
+    lib.device_status()
+    for step in steps:
+        lib.test_set_fault(1 << 20, step)
+        try:
+            t0 = time.perf_counter()
+            lib.paged_attention(q, **c, max_q=max(q_lens), ws=ws)
+            status = lib.device_status()          # synchronizes
+            elapsed = time.perf_counter() - t0
+        finally:
+            lib.test_set_fault(0, -1)
+        assert status & lib.DEV_TIMEOUT, step
+        assert elapsed < 0.5, elapsed
+        out = lib.paged_attention(q, **c, max_q=max(q_lens), ws=ws)
+        B.check(out, B.ref())
+        assert lib.device_status() == 0
