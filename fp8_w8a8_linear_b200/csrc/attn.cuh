@@ -451,7 +451,9 @@ __global__ void __launch_bounds__(kRowsThreads)
   uint32_t* abort_p = reinterpret_cast<uint32_t*>(bars + 2 * SLOTS);
   const uint32_t slot0 = smem_u32(smem), full0 = smem_u32(bars), empty0 = smem_u32(bars + SLOTS);
   const uint32_t abort_w = smem_u32(abort_p);
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = warp_id(), lane = lane_id(), cta = blockIdx.x;
+  // Test hook: CTA 0 skips one slot's load (no arrive, no copies).
+  const int drop = cta == 0 && warp == 4 ? *const_cast<volatile int*>(&g_fault_drop_step) : -1;
   if (threadIdx.x == 0) {
     st_shared_volatile_u32(abort_w, 0u);
     for (int s = 0; s < SLOTS; ++s) {
@@ -465,7 +467,6 @@ __global__ void __launch_bounds__(kRowsThreads)
   __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
-  const int cta = blockIdx.x;
   const AttnRun run = find_run(c.batch, c.heads, cta, gridDim.x, 0, [&](int b) -> HeadUnits {
     if (b >= c.batch) return {0, 0, false};
     const SeqSpan s = seq_span(a, c, b, kRowsBN);
@@ -510,9 +511,10 @@ __global__ void __launch_bounds__(kRowsThreads)
           if (filled >= SLOTS && !mbar_wait_ab(empty0 + 8 * slot, phase ^ 1, abort_w)) ok = false;
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot, bytes);
+          const bool load = filled != drop;
+          if (lane == 0 && load) mbar_arrive_expect_tx(full0 + 8 * slot, bytes);
           __syncwarp();
-          if (mine)
+          if (mine && load)
             tma_load_page(slot0 + slot * C::kSlotBytes + lane * box_bytes, kv ? &tmV : &tmK,
                           full0 + 8 * slot, in_page, w.h, pg, policy);
           ++filled;
@@ -521,11 +523,11 @@ __global__ void __launch_bounds__(kRowsThreads)
       }
       w.next(a, c, n);
     }
-    if (!ok && lane == 0) {
-      // every copy started is waited for (bounded) before the CTA can exit
+    // Every copy started is waited for (bounded) before the CTA can exit, also
+    // where the consumers give up after the last of them is on its way.
+    if (lane == 0)
       for (int i = max(0, filled - SLOTS); i < filled; ++i)
-        mbar_wait(full0 + 8 * (i % SLOTS), (i / SLOTS) & 1);
-    }
+        if (i != drop) mbar_wait(full0 + 8 * (i % SLOTS), (i / SLOTS) & 1);
     return;
   }
 
@@ -1673,8 +1675,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
       }
       w.next(a, c, m, tt, tt1);
     }
+    // Every copy started is waited for (bounded) before the CTA can exit. The
+    // ring's last slots are given back when the products have read them (both
+    // warps end with the same count, so no later load moves their barriers
+    // on); if a consumer gives up before, the copies themselves are waited for.
+    for (int i = max(0, filled - NS); i < filled; ++i) wait(empty0 + 8 * (i % NS), (i / NS) & 1);
     if (!ok && lane == 0) {
-      // every copy started is waited for (bounded) before the CTA can exit
       for (int i = 0; i < NS; ++i)
         if (armed >> i & 1) mbar_wait(full0 + 8 * i, armed_phase >> i & 1);
       if (q_count > 0) mbar_wait(q_full, (q_count - 1) & 1);

@@ -99,12 +99,12 @@ fp8_status fp8_get_device_status(unsigned int* out);
  * `wait_cycles` SM clock cycles (0 restores the default, 2^31 cycles, about
  * 1.1 s at 1965 MHz), and when `drop_step` >= 0 makes CTA 0 of every decode
  * GEMM launch (fp8_rowwise_linear with M <= 128) skip that pipeline step of
- * its K range, and of every bf16_paged_attention launch with max_q * (q_heads
- * / heads) > 16 that load of a key or value tile (or half a tile), in their
- * order: no arrive, no copies, so the MMA's wait for it can end only by the
- * limit. The kernel then records FP8_DEV_TIMEOUT, the producer and MMA
- * roles leave their pipelines, the producer waits for its copies in flight,
- * and the kernel returns (its output is undefined). -1 turns the drop off.
+ * its K range, and CTA 0 of every bf16_paged_attention launch that load of a
+ * key or value tile (or half a tile), counted in their order: no arrive, no
+ * copies, so the wait for it can end only by the limit. The kernel then
+ * records FP8_DEV_TIMEOUT, the producer and MMA roles leave their pipelines,
+ * the producer waits for its copies in flight, and the kernel returns (its
+ * output is undefined). -1 turns the drop off.
  * Synchronizes the device before and after; not for use while other work of
  * this library runs.
  */

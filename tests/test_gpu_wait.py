@@ -53,12 +53,12 @@ def test_a_dropped_stage_times_out_and_the_device_stays_usable(lib, M, N, K, ste
 # items of one key tile. At head_dim 256 a tile has two loads, otherwise one.
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("q_lens,kv_lens,steps", [
-    ([300], [6000], (0, 1, 7)), ([40, 9], [20000, 700], (2, 5)), ([9], [40000], (0, 1, 2, 7)), ([70], [70], (0, 1))])
+    ([300], [6000], (0, 1, 7)), ([40, 9], [20000, 700], (2, 5)), ([9], [38000], (0, 1, 2, 7)), ([70], [70], (0, 1))])
 def test_a_dropped_load_of_a_chunk_times_out_and_the_device_stays_usable(lib, D, q_lens, kv_lens, steps):
     from tests.test_gpu_attention import Batch
 
     B = Batch(q_lens, kv_lens, 16, 4, D, 32)
-    q, c, ws = to_dev(B.q), B.dev(), lib.paged_attention_workspace(D)
+    q, c, ws, ref = to_dev(B.q), B.dev(), lib.paged_attention_workspace(D), B.ref()
     lib.device_status()
     for step in steps:
         lib.test_set_fault(1 << 20, step)
@@ -72,5 +72,12 @@ def test_a_dropped_load_of_a_chunk_times_out_and_the_device_stays_usable(lib, D,
         assert status & lib.DEV_TIMEOUT, step
         assert elapsed < 0.5, elapsed
         out = lib.paged_attention(q, **c, max_q=max(q_lens), ws=ws)
-        B.check(out, B.ref())
+        B.check(out, ref)
         assert lib.device_status() == 0
+
+
+# Few rows: slots of the first lap and of later ones, keys and values, the last load of a CTA with few.
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens,steps", [([1], [50000], (0, 1, 7, 13, 16)), ([4, 1], [64, 64], (0, 1)), ([1] * 9, [9000] * 9, (0, 5, 14))])
+def test_a_dropped_load_of_few_rows_times_out_and_the_device_stays_usable(lib, D, q_lens, kv_lens, steps):
+    test_a_dropped_load_of_a_chunk_times_out_and_the_device_stays_usable(lib, D, q_lens, kv_lens, steps)
