@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_kernel(AppendArgs a, P
     while (b < c.batch && c.cu_q[b + 1] <= t) ++b;
     int64_t at = -1;
     int p = 0;
-    if (b < c.batch) {  // (else a row behind the last sequence)
+    if (b < c.batch && (b > 0 || t >= c.cu_q[0])) {  // (else a row behind the last sequence or in front of the first)
       const int q0 = c.cu_q[b], q1 = c.cu_q[b + 1], len = c.kv_lens[b];
       const int64_t p64 = static_cast<int64_t>(len) - q1 + t;  // len - q_len + (t - q0)
       int32_t page = -1;

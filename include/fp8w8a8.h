@@ -547,11 +547,12 @@ fp8_status fp8_linear_bf16_noalloc(const uint16_t* x, const uint8_t* w8, const f
  *
  * Batch: sequence b owns the rows cu_q[b] .. cu_q[b+1]-1 of the new tokens
  * (q_len = cu_q[b+1] - cu_q[b], 0 allowed) and holds kv_lens[b] keys, the new
- * ones among them: new token i is at position kv_len - q_len + i. Rows at
- * and past cu_q[batch] belong to no sequence and are left as they are. cu_q
- * must not decrease, 0 <= cu_q <= T, and 0 <= kv_len <= max_pages *
- * page_size: a sequence for which this does not hold is skipped (its rows
- * are left as they are) and sets FP8_DEV_BAD_INDEX.
+ * ones among them: new token i is at position kv_len - q_len + i. Rows in
+ * front of cu_q[0], and at and past cu_q[batch], belong to no sequence and are
+ * left as they are. cu_q must not decrease, 0 <= cu_q <= T, and 0 <= kv_len <=
+ * max_pages * page_size: a sequence for which this does not hold is skipped
+ * (its rows are left as they are) and sets FP8_DEV_BAD_INDEX - in the append
+ * where it has a row, which is all that it looks at.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -582,3 +582,33 @@ def test_scores_that_only_their_scale_takes_past_fp32(lib, D, q_lens, kv_lens, H
     out = lib.paged_attention(to_dev(B.q), **B.dev(), scale=32.0, max_q=max(q_lens), lse=lse)
     assert np.isnan(bf16_values(out)[t, 1]).all() and np.isnan(f32(lse)[t, 1])
     assert lib.device_status() == 0
+
+
+def test_part_of_a_batch_by_its_offsets(lib):
+    """cu_q, kv_lens and the table sliced to some sequences of a batch, the rows as they are: the rows in front of the first
+    offset belong to no sequence, like those behind the last."""
+    for q_lens in ([2, 1, 3, 1], [40, 700, 3, 90], [1] * 900):
+        kv_lens = [n + 9 for n in q_lens]
+        B = Batch(q_lens, kv_lens, 4, 2, 64, 16)
+        c, q = B.dev(), to_dev(B.q)
+        k = to_dev(_normal(np.random.default_rng(1), (B.T, 2, 64)))
+        b0, b1 = 1, len(q_lens) - 1
+        r0, r1 = int(B.cu_q[b0]), int(B.cu_q[b1])
+        want = {n: c[n].clone() for n in ("k_cache", "v_cache")}
+        at = _ints(B.table[B.seq, B.pos // 16]).long()[r0:r1], _ints(B.pos % 16).long()[r0:r1]
+        want["k_cache"][at] = want["v_cache"][at] = k[r0:r1]
+        part = {**c, "cu_q": c["cu_q"][b0:b1 + 1].contiguous(), "kv_lens": c["kv_lens"][b0:b1].contiguous(),
+                "page_table": c["page_table"][b0:b1].contiguous()}
+        qo, o = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+        assert lib.kv_append(k, k, **part, q=q, q_out=qo) is qo
+        assert lib.device_status() == 0
+        for n, w in want.items():
+            assert torch.equal(c[n].view(torch.int16), w.view(torch.int16))
+        lib.paged_attention(qo, **part, max_q=max(q_lens), out=o)
+        assert lib.device_status() == 0
+        for y in (qo, o):
+            assert bool((y[:r0] == 7.0).all()) and bool((y[r1:] == 7.0).all())
+        assert torch.equal(qo[r0:r1], q[r0:r1])
+        B.k, B.v = bf16_to_np_bits(c["k_cache"]), bf16_to_np_bits(c["v_cache"])
+        ref = B.ref()
+        assert np.all(np.abs(bf16_values(o) - ref["out"])[r0:r1] <= A.attention_tolerance(ref, 64)[0][r0:r1])
