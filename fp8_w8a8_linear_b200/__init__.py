@@ -654,7 +654,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
 def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = False,
          amplitude: float = 1.0, y: torch.Tensor | None = None):
     """x bf16 [T, heads, head_dim] with the first 2 * len(inv_freq) elements of each head turned by positions int32 [T]
-    (y may be x)."""
+    (y may be x, not another view of its memory)."""
     dev, stream = _current(x, "x")
     shape = x.shape
     ldx = _pitch(x, shape, "x")

@@ -1512,6 +1512,12 @@ fp8_status rows_checked(const void* p, int64_t ld, int64_t heads, int64_t D) {
   return aligned16(p) && ld % 8 == 0 ? FP8_OK : FP8_ERR_ALIGNMENT;
 }
 
+// In place the pitches are one: with two, a token's result lies where another
+// block still reads.
+bool in_place_ok(const void* x, int64_t ldx, const void* y, int64_t ldy, int64_t T) {
+  return x != y || ldx == ldy || T == 1;
+}
+
 }  // namespace
 
 extern "C" fp8_status bf16_rope(const uint16_t* x, int64_t ldx, const int32_t* positions,
@@ -1525,6 +1531,7 @@ extern "C" fp8_status bf16_rope(const uint16_t* x, int64_t ldx, const int32_t* p
   if (T == 0) return FP8_OK;
   if (fp8_status st = rows_checked(x, ldx, heads, head_dim)) return st;
   if (fp8_status st = rows_checked(y, ldy, heads, head_dim)) return st;
+  if (!in_place_ok(x, ldx, y, ldy, T)) return FP8_ERR_INVALID_ARG;
   if (!positions) return FP8_ERR_INVALID_ARG;
   if (!aligned4(positions)) return FP8_ERR_ALIGNMENT;
   DeviceInfo* dev;
@@ -1553,6 +1560,7 @@ extern "C" fp8_status bf16_kv_append(const uint16_t* k, int64_t ldk, const uint1
   if (q) {
     if (fp8_status st = rows_checked(q, ldq, q_heads, kv->head_dim)) return st;
     if (fp8_status st = rows_checked(q_out, ldq_out, q_heads, kv->head_dim)) return st;
+    if (!in_place_ok(q, ldq, q_out, ldq_out, T)) return FP8_ERR_INVALID_ARG;
   }
   DeviceInfo* dev;
   if (fp8_status st = device_info(&dev)) return st;

@@ -605,7 +605,8 @@ fp8_status bf16_rope(const uint16_t* x, int64_t ldx, const int32_t* positions,
  * cache, the keys turned by their positions as in bf16_rope (rotary_dim 0:
  * not at all, inv_freq may be NULL). With q not NULL the queries are turned
  * in the same launch: q_out = rope(q), as bf16_rope with the tokens'
- * positions; q_out may be q. kv_lens counts the new tokens already.
+ * positions; q_out may be q (with the same pitch). kv_lens counts the new
+ * tokens already.
  *   k, v [T, heads, head_dim] bf16 (pitch ldk, ldv); q, q_out [T, q_heads,
  *   head_dim] bf16 (pitch ldq, ldq_out).
  * A new token whose position is negative (q_len > kv_len) or whose page is

@@ -103,3 +103,14 @@ def test_binding_refuses_host_tensors_and_wrong_types():
     with pytest.raises(ValueError):
         f.paged_attention(x, x[None], x[None], torch.zeros((1, 1), dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                           torch.zeros(1, dtype=torch.int32))
+
+
+def test_in_place_takes_one_pitch(raw):
+    """y = x with another pitch would write rows that other blocks still read."""
+    def rope(T, ldx, ldy, y=FAKE):
+        return raw.bf16_rope(FAKE, ldx, FAKE, FAKE, T, 4, 64, 32, 0, 1.0, y, ldy, None)
+
+    def append(T, ldq, ldqo, qo=FAKE):
+        return raw.bf16_kv_append(FAKE, 128, FAKE, 128, FAKE, ldq, qo, ldqo, 4, T, _kv(), FAKE, 64, 0, 1.0, None)
+
+    assert rope(4, 256, 320) == rope(4, 512, 256) == append(3, 256, 264) == append(2, 512, 256) == INVALID
