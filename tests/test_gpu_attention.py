@@ -612,3 +612,83 @@ def test_part_of_a_batch_by_its_offsets(lib):
         B.k, B.v = bf16_to_np_bits(c["k_cache"]), bf16_to_np_bits(c["v_cache"])
         ref = B.ref()
         assert np.all(np.abs(bf16_values(o) - ref["out"])[r0:r1] <= A.attention_tolerance(ref, 64)[0][r0:r1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 24, 64])
+@pytest.mark.parametrize("q_lens,window", [([1, 1, 1], 100), ([1, 1, 2], 1), ([70, 1, 9], 64), ([40, 200, 3], 500)])
+def test_table_entries_before_the_window_are_not_looked_at(lib, D, page, q_lens, window):
+    """A server has given the pages away that lie wholly before the first key that any new token sees: their entries are
+    negative or past the end, and no flag is set."""
+    B = Batch(q_lens, [900, 1400, 33], 4, 2, D, page)
+    ref, gone = B.ref(window), 0
+    for b, n in enumerate(q_lens):
+        first = max(0, B.kv_lens[b] - n - window + 1) // page
+        B.table[b, :first] = [-7 if i % 2 else B.pages + 5 for i in range(first)]
+        gone += first
+    assert gone > 0
+    out = lib.paged_attention(to_dev(B.q), **B.dev(), window=window, max_q=max(q_lens))
+    B.check(out, ref)
+    assert lib.device_status() == 0
+
+
+def test_offsets_past_2_to_the_32_elements(lib):
+    """k and v are the halves of one array of more than 2^32 elements, the pages in use at its end."""
+    page, Hkv, D = 64, 8, 256
+    pages = (1 << 32) // (2 * page * Hkv * D) + 40
+    big = torch.empty((pages, 2, page, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    for q_lens in ([1, 1], [90, 2]):
+        B = Batch(q_lens, [500, 200], 16, Hkv, D, page)
+        c, at = B.dev(), pages - B.pages
+        assert at * big.stride(0) >= 1 << 32
+        for i, n in enumerate(("k_cache", "v_cache")):
+            big[at:, i] = c[n]
+            c[n] = big[:, i]
+        c["page_table"] = torch.where(c["page_table"] >= 0, c["page_table"] + at, c["page_table"])
+        B.check(lib.paged_attention(to_dev(B.q), **c, max_q=max(q_lens)), B.ref())
+        k = _normal(np.random.default_rng(8), (B.T, Hkv, D))
+        lib.kv_append(to_dev(k), to_dev(k), **c)
+        rows = _ints(B.table[B.seq, B.pos // page] + at).long(), _ints(B.pos % page).long()
+        for n in ("k_cache", "v_cache"):
+            assert np.array_equal(bf16_to_np_bits(c[n][rows]), k)
+    assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_chunks_and_single_tokens_are_both_within_the_tolerance(lib, D):
+    """A prompt appended and attended whole, in uneven chunks, and token by token: the same cache bit for bit, every row of
+    every way within its own tolerance of the float64 form."""
+    T, Hq, Hkv, page = 150, 8, 2, 16
+    rng = np.random.default_rng(12)
+    q, k, v = (to_dev(_normal(rng, (T, h, D))) for h in (Hq, Hkv, Hkv))
+    f = lib.rope_frequencies(D)[0].cuda()
+    table = rng.permutation(10)[None]
+    caches = []
+    for steps in ([T], [1] * T, [70, 3, 1, 60, 16]):
+        kc, vc = (torch.zeros((10, page, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        out, qrs, t = [], [], 0
+        for n in steps:
+            batch = (kc, vc, _ints(table), _ints([0, n]), _ints([t + n]))
+            qrs.append(lib.kv_append(k[t:t + n], v[t:t + n], *batch, inv_freq=f, q=q[t:t + n]))
+            out.append(lib.paged_attention(qrs[-1], *batch, max_q=n))
+            t += n
+        ref = A.paged_attention(bf16_values(torch.cat(qrs)), bf16_values(kc), bf16_values(vc), table, [0, T], [T], D ** -0.5)
+        tol, _ = A.attention_tolerance(ref, D)
+        err = np.abs(bf16_values(torch.cat(out)) - ref["out"])
+        assert np.all(err <= tol), (len(steps), float((err / tol).max()))
+        caches.append((torch.cat(qrs), kc, vc))
+    for other in caches[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(caches[0], other))
+    assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_lens", [[1, 2, 1], [100, 60, 3]])
+def test_one_head_of_keys_expanded_to_several(lib, D, q_lens):
+    """The cache's heads are one head, repeated by a stride of 0."""
+    B = Batch(q_lens, [200, 61, 90], 8, 1, D, 16)
+    c, q = B.dev(), to_dev(B.q)
+    wide = {**c, **{n: c[n].expand(-1, -1, 4, -1) for n in ("k_cache", "v_cache")}}
+    assert wide["k_cache"].stride(2) == 0
+    B.check(lib.paged_attention(q, **wide, max_q=max(q_lens)), B.ref())
+    assert lib.device_status() == 0
