@@ -692,3 +692,45 @@ def test_one_head_of_keys_expanded_to_several(lib, D, q_lens):
     assert wide["k_cache"].stride(2) == 0
     B.check(lib.paged_attention(q, **wide, max_q=max(q_lens)), B.ref())
     assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2], [40, 30]])
+def test_a_cache_without_pages(lib, q_lens):
+    """No page and no key anywhere: every token sees nothing."""
+    for D in (64, 128, 256):
+        kc = torch.empty((0, 16, 2, D), dtype=torch.bfloat16, device="cuda")
+        T = sum(q_lens)
+        q, lse = torch.ones((T, 4, D), dtype=torch.bfloat16, device="cuda"), torch.ones((T, 4), device="cuda")
+        table = torch.empty((2, 0), dtype=torch.int32, device="cuda")
+        out = lib.paged_attention(q, kc, kc.clone(), table, _ints([0, q_lens[0], T]), _ints([0, 0]), max_q=max(q_lens), lse=lse)
+        assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+        assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [5, 3000])
+def test_append_from_fused_rows_in_place(lib, T):
+    """q, k and v are slices of one row; the queries are turned in place."""
+    Hq, Hkv, D, page = 6, 2, 64, 16
+    rng = np.random.default_rng(T)
+    x = _normal(rng, (T, Hq + 2 * Hkv + 1, D))
+    f = lib.rope_frequencies(D)[0]
+    n = -(-T // page)
+    kc, vc = (torch.zeros((n, page, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rows = to_dev(x)
+    q, k, v = rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:Hq + 2 * Hkv]
+    assert lib.kv_append(k, v, kc, vc, _ints(np.arange(n)[None]), _ints([0, T]), _ints([T]), inv_freq=f.cuda(), q=q, q_out=q) is q
+    for got, a, b in ((q, 0, Hq), (kc.view(-1, Hkv, D)[:T], Hq, Hq + Hkv)):
+        y, size = A.rope(A.bf16_f64(x[:, a:b]), np.arange(T), f.numpy())
+        assert np.all(np.abs(bf16_values(got) - y) <= A.rope_tolerance(y, size))
+    assert np.array_equal(bf16_to_np_bits(vc.view(-1, Hkv, D)[:T]), x[:, Hq + Hkv:Hq + 2 * Hkv])
+    assert np.array_equal(bf16_to_np_bits(rows)[:, Hq:], x[:, Hq:])
+    assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_thousands_of_sequences(lib, D):
+    rng = np.random.default_rng(D)
+    kv = rng.integers(0, 60, 4500)
+    _run(lib, Batch([1] * 4500, kv.tolist(), 4, 2, D, 8))
+    q = rng.integers(0, 4, 4500)
+    _run(lib, Batch(q.tolist(), (q + kv).tolist(), 8, 1, D, 8), window=40)
