@@ -47,6 +47,7 @@ struct AttnArgs {
   int window;        // keys a token sees at most
   float scale_log2;  // scale * log2(e)
   int box_rows;      // tokens of a page that one TMA box brings
+  int drop;          // test hook: the load that CTA 0 skips (no arrive, no copies); -1: none
   // workspace: parts' o [2 per CTA][rows][D], their (maximum, sum)
   // [2 per CTA][rows], and per CTA what to join
   float* part_o;
@@ -452,8 +453,6 @@ __global__ void __launch_bounds__(kRowsThreads)
   const uint32_t slot0 = smem_u32(smem), full0 = smem_u32(bars), empty0 = smem_u32(bars + SLOTS);
   const uint32_t abort_w = smem_u32(abort_p);
   const int warp = warp_id(), lane = lane_id(), cta = blockIdx.x;
-  // Test hook: CTA 0 skips one slot's load (no arrive, no copies).
-  const int drop = cta == 0 && warp == 4 ? *const_cast<volatile int*>(&g_fault_drop_step) : -1;
   if (threadIdx.x == 0) {
     st_shared_volatile_u32(abort_w, 0u);
     for (int s = 0; s < SLOTS; ++s) {
@@ -480,6 +479,7 @@ __global__ void __launch_bounds__(kRowsThreads)
     const uint64_t policy = l2_policy_evict_first();
     const int rows = a.box_rows, boxes = kRowsBN / rows;
     const uint32_t box_bytes = static_cast<uint32_t>(rows) * D * 2;
+    const int drop = cta == 0 ? a.drop : -1;
     int slot = 0, filled = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -1482,8 +1482,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   const uint32_t q_smem = smem_u32(smem), slot0 = smem_u32(slots);
   const int warp = warp_id(), lane = lane_id();
   constexpr int kMmaWarp = NT * 4, kLoadWarp = NT * 4 + 1;  // and kLoadWarp + 1
-  // Test hook: CTA 0 skips one slot's load (no arrive, no copies).
-  const int drop = blockIdx.x == 0 && warp >= kLoadWarp ? *const_cast<volatile int*>(&g_fault_drop_step) : -1;
 
   if (threadIdx.x == 0) {
     st_shared_volatile_u32(abort_w, 0u);
@@ -1547,6 +1545,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
     const int piece = lane / groups, grp = lane % groups;
     const uint32_t dst0 = slot0 + grp * (pieces * box_bytes) + piece * box_bytes;
     const bool has_box = lane < pieces * groups;
+    const int drop = blockIdx.x == 0 ? a.drop : -1;
     int slot = 0, filled = 0;
     uint32_t phase = 0, q_count = 0;
     uint32_t armed = 0, armed_phase = 0;  // this warp's slots and the phases that its last loads fill

@@ -33,6 +33,7 @@ struct DeviceInfo {
   int smem_optin = 0;     // largest dynamic shared memory a block may opt into
   int pair_clusters = 0;  // co-resident 2-CTA clusters of the pair GEMM
   int attn_rows_ctas[3] = {};  // co-resident CTAs of attn_rows_kernel, head_dim 64, 128, 256
+  int drop_step = -1;          // fp8_test_set_fault's, for the kernels that get it as an argument
   bool supported = false;
   bool attrs_set = false;
 };
@@ -871,6 +872,9 @@ fp8_status fp8_test_set_fault(int64_t wait_cycles, int32_t drop_step) {
   if (wait_cycles < 0 || drop_step < -1) return FP8_ERR_INVALID_ARG;
   const long long lim = wait_cycles == 0 ? fp8k::kWaitCycles : static_cast<long long>(wait_cycles);
   const int drop = drop_step;
+  DeviceInfo* dev;
+  if (fp8_status st = device_info(&dev)) return st;
+  dev->drop_step = drop;
   if (cudaDeviceSynchronize() != cudaSuccess) return FP8_ERR_CUDA;
   if (cudaMemcpyToSymbol(fp8k::g_wait_limit, &lim, sizeof(lim)) != cudaSuccess ||
       cudaMemcpyToSymbol(fp8k::g_fault_drop_step, &drop, sizeof(drop)) != cudaSuccess)
@@ -1703,6 +1707,7 @@ extern "C" fp8_status bf16_paged_attention(const uint16_t* q, int64_t ldq, int64
   a.max_q = static_cast<int>(max_q <= 0 ? T : std::min(max_q, T));
   a.window = static_cast<int>(window > 0 ? std::min(window, kMaxTokens) : kMaxTokens);
   a.scale_log2 = scale * 1.44269504088896341f;
+  a.drop = dev->drop_step;
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.part_o = reinterpret_cast<float*>(w);
   a.part_ml = reinterpret_cast<float2*>(w + need.o);

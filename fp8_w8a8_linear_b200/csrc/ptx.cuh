@@ -61,9 +61,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 constexpr long long kWaitCycles = 1ll << 31;
 __device__ long long g_wait_limit = kWaitCycles;
 
-// Test hook (fp8_test_set_fault): when >= 0, CTA 0 of the decode GEMM, or of
-// paged attention, skips this pipeline step's stage (no arrive, no loads), so
-// the wait for it can only end by its time limit.
+// Test hook (fp8_test_set_fault): when >= 0, CTA 0 of the decode GEMM skips
+// this pipeline step's stage (no arrive, no loads), so the MMA's wait on it
+// can only end by its time limit.
 __device__ int g_fault_drop_step = -1;
 
 // Waits for the phase with the given parity to complete. Returns false (and
