@@ -719,7 +719,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     lse: torch.Tensor | None = None):
     """Attention of the new tokens' q bf16 [T, q_heads, head_dim] over the paged cache (see kv_append), causal, over the
     last ``window`` keys when window > 0; scale defaults to head_dim^-0.5. max_q: no sequence has more new tokens
-    (None: T). lse fp32 [T, q_heads] receives ln sum exp of the scores when given. Returns out bf16 [T, q_heads,
+    (None: T). Give it for decoding: up to max_q * q_heads / heads = 16 the call takes the kernel made for few rows, which
+    for 64 requests of one token over short contexts halves its time. page_size is a multiple of 8. lse fp32 [T, q_heads] receives ln sum exp of the scores when given. Returns out bf16 [T, q_heads,
     head_dim], which must not overlap q; rows behind cu_q[batch] stay as they are."""
     dev, stream = _current(q, "q")
     shape = q.shape

@@ -5,9 +5,11 @@
 // p the position of the new token, kv_len - q_len + its place among the new
 // tokens. One pass over the keys with the running maximum and sum of the
 // softmax, in base 2 (the scale times log2 e is folded into the exponent's
-// argument); scores, statistics and o in fp32; the probabilities go to bf16
-// for their product with v (|p| <= 1 relative to the row's maximum, so each
-// is off by 2^-8 of itself at most), o is rounded once to bf16.
+// argument); scores, statistics and o in fp32. The probabilities go to bf16
+// for their product with v, as the tensor core takes them: each is off by 2^-8
+// of itself at most, while their sum adds the unrounded ones (lse stays an
+// fp32 value). o is rounded once to bf16. Against 64 bits the relative error of
+// o, root mean square, is 1.8e-3 to 2.3e-3; that last rounding alone is 1.7e-3.
 //
 // Work. The query heads that share a key/value head are taken together: row
 // r of an item is new token r / G, head r % G of the group, so keys and
@@ -16,16 +18,23 @@
 // CTA: a ragged batch, a single long context and a full batch all load the
 // device evenly. An item cut between CTAs leaves an unnormalised o with its
 // maximum and sum for each part in the workspace, and a join kernel adds the
-// parts in order. The cut depends on the lengths and the grid alone, so
-// results are bit-reproducible. Every warp finds its CTA's run by itself from
+// parts in order. The cut depends on the lengths, the heads, the window, max_q
+// (which picks the kernel) and the grid alone, so results are
+// bit-reproducible. Every warp finds its CTA's run by itself from
 // the lengths, so a captured graph follows lengths that change.
 //
 // Two kernels: attn_rows_kernel for items of at most 16 rows (max_q * G <= 16,
 // one mma.sync row tile), attn_chunk_kernel for more, on tcgen05. The first is
-// the one whose items cost little: 64 requests of one token (G = 4) over up to
-// 300 keys 21.5 us, with the second 50.2; over up to 8K keys, where both are
-// bound by the cache's bytes, 212 and 216 us; 24 requests of 4 tokens (16 rows)
-// 56.8 and 54.4.
+// the one whose items cost little, and its cost grows with the rows; the
+// second's does not. Measured, first / second, us, batches of 64 requests:
+//              up to 300 keys                up to 4096 keys
+//   rows       4           8           16           4          8          16
+//   D 64   16.4/41.1   18.3/41.2   22.5/41.2    85/98      88/98      92/99
+//   D 128  21.8/45.4   24.6/45.3   30.0/45.5   117/122    121/123    127/125
+//   D 256  25.6/44.6   27.2/43.8   31.8/44.0   115/125    120/126    131/128
+// At exactly 16 rows over long contexts of wide heads the second is ahead by
+// some 2 % (single runs 8 %), over short ones the first by a third, so the rule
+// takes the first.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -126,8 +135,9 @@ __device__ __forceinline__ long long warp_scan(long long v) {
   return v;
 }
 
-// Units of a run from which on items count their own cost (14: a draft check
-// 37.6 us without, 36.5 with); below, a run is about as short as the cost, and
+// Units of a run from which on items count their own cost (an 8K prompt, runs
+// of some 470 units: 541 us if they never do, 486 if they do; a draft check,
+// runs of 14: 36.5 and 35.1); below, a run is about as short as the cost, and
 // whole tiles decide.
 constexpr int kExtraRun = 8;
 
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(256) attn_join_chunk_kernel(AttnArgs a) {
 // the main loop has no exchange between warps; they join through shared
 // memory at an item's end. 64 requests of up to 8K keys (8 key/value heads of
 // 128) take 212 us, 6.1 TB/s, 0.95 of the copy rate; one request's 120K keys (4
-// of 256) 87 us, 5.7 TB/s; one of 1000 keys 8.4 us, which is latency: two
+// of 256) 87 us, 5.7 TB/s; one of 1000 keys 8.5 us, which is latency: two
 // launches, a look at the lengths, two tiles and the join.
 constexpr int kRowsBN = 64;
 constexpr int kRowsThreads = 160;
@@ -755,8 +765,9 @@ __global__ void __launch_bounds__(kRowsThreads)
 // the last time (the factor cancels in the end, and 2^8 times a probability is
 // as exact in bf16 and far from overflow in the sums): after the first tiles
 // hardly ever, so the softmax threads do it themselves.
-// Bound: 8192 tokens of 32 heads (head_dim 128, 8 key/value heads) take 495 us,
-// 1.11 PFLOP/s, at the power limit. Per key tile of two row tiles that is some
+// Bound: 8192 tokens of 32 heads (head_dim 128, 8 key/value heads) take 500 us,
+// 1.10 PFLOP/s, in short bursts at 1965 MHz, and 573 us call after call, where
+// the 1000 W limit holds the clock at 1660 MHz. Per key tile of two row tiles that is some
 // 3500 cycles, of which the tensor core works 2048 and the exponentials (4 a
 // cycle and scheduler) 2048: what is left is the chain above, which with the
 // two row tiles that TMEM holds (S, P and O of a third do not fit) is not quite
@@ -1529,7 +1540,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::kThreads, 1)
   } else if (warp == kMmaWarp) {
     if (lane == 0) chunk_issue<D, PACKED>(a, c, w, tt1, tmem, q_smem, slot0, full0, abort_w);
   } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
-    
     // ------------------------------------------------------------- loads
     // One warp for queries and keys, one for values; they share the ring,
     // whose order both know, and each passes over the other's slots.
